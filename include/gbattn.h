@@ -52,6 +52,15 @@ extern "C" {
 #define GBATTN_ERR_FLAGS (-10)      /* attn_fwd_ex: unknown bits in flags                    */
 #define GBATTN_ERR_WORKSPACE (-11)  /* attn_fwd_host: device workspace too small             */
 #define GBATTN_ERR_SCRATCH (-12)    /* attn_bwd_noalloc: shape needs more than its fixed buffer */
+#define GBATTN_ERR_DTYPE (-13)      /* dtype is neither GBATTN_F16 nor GBATTN_BF16           */
+#define GBATTN_ERR_STRIDE (-14)     /* a stride is negative or not a multiple of 8 elements,
+                                       or the pages' strides make their rows overlap         */
+#define GBATTN_ERR_ROTARY (-15)     /* rotary is not a multiple of 16 in [0, d], or norm
+                                       weights or frequencies are incomplete                 */
+#define GBATTN_ERR_PAGES (-16)      /* a page size that is not a multiple of 8, or (copy) a
+                                       page number outside the cache                         */
+#define GBATTN_ERR_HEADS (-17)      /* Hq is not a multiple of Hkv                           */
+#define GBATTN_ERR_MEMORY (-18)     /* no host memory                                        */
 
 /* Device-side status codes reported by attn_last_device_error() (positive). */
 #define GBATTN_DEV_TIMEOUT_LOAD 1    /* the TMA producer's wait for a free buffer timed out  */
@@ -61,6 +70,8 @@ extern "C" {
 #define GBATTN_DEV_TIMEOUT_PROBE 5   /* the self-test wait of attn_debug_wait_probe ran out */
 #define GBATTN_DEV_TIMEOUT_MERGE 6   /* attn_decode: waiting for the other CTAs' partials ran out */
 #define GBATTN_DEV_SMEM_ALIGN 7      /* attn_bwd: dynamic shared memory not 1 KB aligned (kernel skipped) */
+#define GBATTN_DEV_BAD_PAGE 8        /* a page number outside the cache within a sequence's length */
+#define GBATTN_DEV_BAD_LENGTH 9      /* a length negative, beyond the page table, or below the new tokens */
 
 /*
  * attn_fwd -- the fused forward pass.
@@ -252,6 +263,126 @@ long long attn_decode_workspace_bytes(int B, int H, int d);
  * Returns 0 or a negative GBATTN_ERR_* code.
  */
 int attn_debug_decode_plan(int B, int H, int L, int d, int sm_count, int max_ranks, int grouped, int *out);
+
+/* ------------------------------------------------------------------------------------
+ * Operators beside the attention kernels: rotary positions and per-head norms of queries
+ * and keys, and a paged key/value cache.  What they share, besides the conventions above:
+ *   - Values are fp16 or bf16 (`dtype`), the same for every tensor of a call.
+ *   - Rows (queries, keys, values, upstream gradients) are given by a pointer and three
+ *     element strides: element (b, h, l, i) lies at b * sb + h * sh + l * sl + i.  Strides are
+ *     non-negative multiples of 8; inputs may repeat elements (stride 0).  So a projection's
+ *     output [B, L, Hq + 2 Hkv, d] is read where it lies.  Outputs are contiguous.
+ *   - A cache is two arrays of `pages` pages, for keys and for values, each page holding
+ *     `page` slots (a multiple of 8) of Hkv heads: element (page, head, slot, i) lies at
+ *     page * sp + head * sh + slot * ss + i in both.  Strides are multiples of 8; the page's
+ *     stride is at least a page's extent; head and slot may come in either order.
+ *   - Sequence b's token j lies in slot j % page of page table[b * table_stride + j / page],
+ *     0 <= j < lengths[b].  `table` (int32, table_width entries a sequence) and `lengths`
+ *     (int32) are device memory; entries behind a sequence's last token are not read.
+ *     A length that is negative or beyond the table, or a page number outside the cache
+ *     within the length, is recorded in the device status word (GBATTN_DEV_BAD_LENGTH,
+ *     GBATTN_DEV_BAD_PAGE); nothing outside the given arrays is read or written.
+ * B, H, L and d: positive, d 64, 128, 256 or 512; 16-byte aligned pointers (inv_freq 8, int32
+ * arrays 4).  `rotary`: rotated elements of a head, a multiple of 16 in [0, d].
+ */
+#define GBATTN_F16 0
+#define GBATTN_BF16 1
+
+/*
+ * attn_rope -- norms (optional) and rotary positions of queries and keys, in one pass.  For a
+ * row x at position p, and w the norm's weight,
+ *     y = x * rsqrt(mean(x^2) + eps) * w       (y = x when q_weight and k_weight are NULL)
+ *     z_i = factor (y_i cos a - y_j sin a),  z_j = factor (y_j cos a + y_i sin a),  a = p inv_freq[r]
+ * for the r-th pair (i, j), r < rotary / 2: (r, r + rotary / 2), or (2r, 2r + 1) when
+ * `interleaved`; z = y behind the first `rotary` elements.
+ *   q, k       : rows [B, Hq, L, d] and [B, Hkv, L, d]; k may be NULL with Hkv = 0.
+ *   q_out, k_out : contiguous [B, Hq, L, d] and [B, Hkv, L, d]; overlap no input.
+ *   inv_freq   : const double [rotary / 2], device (64 bits: frequencies times positions of
+ *                10^6 and more keep their accuracy).  NULL when rotary is 0.
+ *   positions  : const int32 [B, L] with row stride positions_stride (0: one row for all),
+ *                or NULL: 0 .. L-1.
+ *   q_weight, k_weight : [d] of type dtype, both or neither (k_weight NULL without k).
+ *   factor     : finite, > 0.  eps: finite, >= 0.
+ * Arithmetic in fp32 (angles reduced in 64-bit integers), rounded once.
+ */
+int attn_rope(const void *q, long long q_sb, long long q_sh, long long q_sl, const void *k, long long k_sb,
+              long long k_sh, long long k_sl, void *q_out, void *k_out, const double *inv_freq, int rotary,
+              int interleaved, float factor, const int *positions, long long positions_stride, const void *q_weight,
+              const void *k_weight, float eps, int dtype, int B, int Hq, int Hkv, int L, int d, void *stream);
+
+/*
+ * attn_rope_bwd -- the gradients of attn_rope: from dq_up, dk_up (gradients of q_out, k_out;
+ * rows) those of q and k (dq, dk: contiguous), and, with norms, of the weights (dq_weight,
+ * dk_weight: fp32 [d], summed over all rows and heads).  With dy the upstream gradient
+ * turned by -a (times factor), xh = x rsqrt(mean(x^2) + eps) and g = dy w:
+ *     dx = rsqrt(mean(x^2) + eps) (g - xh mean(g xh)),   dw = sum dy xh;   dx = dy without norms.
+ *   q, k       : attn_rope's inputs, read with norms only (else may be NULL).
+ *   workspace  : with norms, attn_rope_bwd_workspace_bytes(d) bytes, 16-byte aligned.
+ * Sums are taken in a fixed order: the same call gives the same bits.
+ */
+int attn_rope_bwd(const void *dq_up, long long dq_sb, long long dq_sh, long long dq_sl, const void *dk_up,
+                  long long dk_sb, long long dk_sh, long long dk_sl, const void *q, long long q_sb, long long q_sh,
+                  long long q_sl, const void *k, long long k_sb, long long k_sh, long long k_sl, void *dq, void *dk,
+                  float *dq_weight, float *dk_weight, const double *inv_freq, int rotary, int interleaved, float factor,
+                  const int *positions, long long positions_stride, const void *q_weight, const void *k_weight, float eps,
+                  void *workspace, int dtype, int B, int Hq, int Hkv, int L, int d, void *stream);
+
+/* Bytes of attn_rope_bwd's workspace (host-only; GBATTN_ERR_HEAD_DIM for another d). */
+long long attn_rope_bwd_workspace_bytes(int d);
+
+/*
+ * attn_cache_append -- new tokens' keys and values into a paged cache, and, with `rotary` or
+ * norm weights, norms and rotary positions of the keys (and of the queries) on the way.
+ * Sequence b's new tokens are the first counts[b] of its L rows (counts NULL: all L), at
+ * positions lengths[b] - counts[b] .. lengths[b] - 1: `lengths` already counts them, so that
+ * the same array serves attn_decode_paged afterwards.
+ *   k, v       : rows [B, Hkv, L, d].  q: rows [B, Hq, L, d], or NULL with Hq = 0.
+ *   q_out      : contiguous [B, Hq, L, d]: the turned queries, zeros in rows t >= counts[b].
+ *   others     : as for attn_rope.  q_weight is NULL without q.
+ * Only the new tokens' slots are written.  A sequence with a bad length or count is left
+ * out as a whole (its q_out is zero), a token whose page is outside the cache is left out.
+ * Two tokens of one call that share a slot (a page in two sequences' tables) leave either's
+ * values there.
+ */
+int attn_cache_append(const void *k, long long k_sb, long long k_sh, long long k_sl, const void *v, long long v_sb,
+                      long long v_sh, long long v_sl, const void *q, long long q_sb, long long q_sh, long long q_sl,
+                      void *q_out, void *k_pages, void *v_pages, long long page_stride, long long head_stride,
+                      long long slot_stride, int pages, int page, const int *table, long long table_stride,
+                      int table_width, const int *lengths, const int *counts, const double *inv_freq, int rotary,
+                      int interleaved, float factor, const void *q_weight, const void *k_weight, float eps, int dtype,
+                      int B, int Hq, int Hkv, int L, int d, void *stream);
+
+/*
+ * attn_cache_copy -- copy n pages of a cache, keys and values: for i = 0 .. n-1, in this order,
+ * page src[i] to page dst[i].  src and dst are HOST arrays (read before the call returns; a
+ * captured graph repeats these copies).  The result is that of copying one page after the
+ * other, also where a page occurs more than once: pairs that depend on one another are put
+ * into launches of their own.  Numbers outside [0, pages): GBATTN_ERR_PAGES, nothing is
+ * copied.  n = 0 is allowed.
+ */
+int attn_cache_copy(void *k_pages, void *v_pages, long long page_stride, long long head_stride, long long slot_stride,
+                    int pages, int page, int Hkv, int d, const int *src, const int *dst, int n, void *stream);
+
+/*
+ * attn_decode_paged -- decoding over a paged cache: one query row per sequence and head
+ * against the sequence's lengths[b] tokens; query head h uses key head h / (Hq / Hkv).
+ *     o[b,h,:] = sum_j softmax_j(scale * q[b,h] . k_j) v_j,   lse[b,h] = log sum_j exp(scale * q[b,h] . k_j)
+ * An empty sequence gives o = 0 and lse = -inf.  A bad length is taken as 0 (negative) or as
+ * the table's end; a page outside the cache counts as keys and values of zeros.
+ *   q          : [B, Hq, d] by strides q_sb, q_sh.  o: contiguous [B, Hq, d]; lse: fp32 [B, Hq].
+ *   workspace  : attn_decode_paged_workspace_bytes(Hq, Hkv, d) bytes, 16-byte aligned,
+ *                overlapping no input or output; its contents on entry do not matter.  Calls
+ *                that can run at the same time need one each.
+ *   Hq         : a multiple of Hkv (else GBATTN_ERR_HEADS).  scale: finite, > 0.
+ * What lies behind a sequence's last token in its last page does not matter (NaN included).
+ */
+int attn_decode_paged(const void *q, long long q_sb, long long q_sh, const void *k_pages, const void *v_pages,
+                      long long page_stride, long long head_stride, long long slot_stride, int pages, int page,
+                      const int *table, long long table_stride, int table_width, const int *lengths, void *o,
+                      float *lse, void *workspace, int dtype, int B, int Hq, int Hkv, int d, float scale, void *stream);
+
+/* Bytes of attn_decode_paged's workspace (host-only; negative GBATTN_ERR_* on bad arguments). */
+long long attn_decode_paged_workspace_bytes(int Hq, int Hkv, int d);
 
 /*
  * attn_debug_scores -- test hook: the raw scaled logits s[b,h,i,j] = scale * q_i . k_j

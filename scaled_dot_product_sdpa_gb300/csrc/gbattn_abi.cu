@@ -15,6 +15,7 @@
 #include <queue>
 #include <vector>
 
+#include "abi_host.cuh"
 #include "attn_bwd.cuh"
 #include "attn_decode.cuh"
 #include "attn_fwd_kernel.cuh"
@@ -485,6 +486,25 @@ void decode_plan(long long BH, int L, int d, int sm_count, int max_ranks, bool g
 int dec_dim_index(int d) { return d == 64 ? 0 : d == 128 ? 1 : d == 256 ? 2 : 3; }
 
 }  // namespace
+
+int abi_device(int *sm_count, unsigned **status) {
+  DevInfo *di = nullptr;
+  const int rc = device_info(&di);
+  if (rc != GBATTN_OK) return rc;
+  *sm_count = di->sm_count;
+  *status = di->status;
+  return GBATTN_OK;
+}
+
+int abi_encode(CUtensorMap *tm, bool bf16, int rank, const void *ptr, const cuuint64_t *dims, const cuuint64_t *strides,
+               const cuuint32_t *box) {
+  const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
+  const CUresult r = g_encode(tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                              static_cast<cuuint32_t>(rank), const_cast<void *>(ptr), dims, strides, box, estride,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? GBATTN_OK : GBATTN_ERR_TENSORMAP;
+}
 }  // namespace gbattn
 
 using namespace gbattn;
@@ -912,6 +932,14 @@ extern "C" const char *attn_strerror(int code) {
     case GBATTN_ERR_FLAGS: return "flags holds bits that name no option";
     case GBATTN_ERR_WORKSPACE: return "the device workspace is smaller than attn_fwd_host_workspace_size()";
     case GBATTN_ERR_SCRATCH: return "the shape needs more workspace than attn_bwd_noalloc's fixed buffer holds";
+    case GBATTN_ERR_DTYPE: return "dtype is neither GBATTN_F16 nor GBATTN_BF16";
+    case GBATTN_ERR_STRIDE: return "a stride is negative or not a multiple of 8 elements, or the pages' strides make their rows overlap";
+    case GBATTN_ERR_ROTARY: return "the rotary width is not a multiple of 16 up to head_dim, or its norm weights or frequencies are incomplete";
+    case GBATTN_ERR_PAGES: return "a page size is not a multiple of 8, or a page number lies outside the cache";
+    case GBATTN_ERR_HEADS: return "the query heads are not a multiple of the key heads";
+    case GBATTN_ERR_MEMORY: return "no host memory";
+    case GBATTN_DEV_BAD_PAGE: return "device: a page table names a page outside the cache within a sequence's length";
+    case GBATTN_DEV_BAD_LENGTH: return "device: a sequence's length is negative, beyond its page table, or below its new tokens";
     case GBATTN_DEV_TIMEOUT_LOAD: return "device: the TMA producer's wait timed out";
     case GBATTN_DEV_TIMEOUT_MMA: return "device: the MMA issuer's wait timed out";
     case GBATTN_DEV_TIMEOUT_SOFTMAX: return "device: a softmax warp's wait timed out";
