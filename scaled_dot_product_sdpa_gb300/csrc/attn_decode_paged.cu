@@ -1,7 +1,27 @@
-// attn_decode_paged.cu -- decoding over a paged cache: one block per sequence and query head,
-// whose eight warps take the keys in turn, each with its own running maximum and sum, and
-// join them at the end.
+// attn_decode_paged.cu -- decoding over a paged cache (see attn_decode_paged.cuh).
+//
+// Bound by the HBM reads of K and V: a key head's rows are used by G query heads, 2 G FLOPs per
+// byte, more than the CUDA cores can do at HBM speed from G = 4 on.  So both products run on
+// the tensor cores, in the orientation that makes the keys the 128-row operand:
+//     S^T [128 keys x N heads]  = K [128 x d] Q^T           (K as TMA wrote it, K-major)
+//     O^T [128 columns x 2N]   += V^T [128 x 128 keys] P^T  (V as TMA wrote it, MN-major)
+// No byte of K or V passes through a register, and a softmax thread owns one key with all its
+// heads.  The weights P enter the second product as two 16-bit parts, P = hi + lo, in separate
+// columns (N heads are padded to 8 while a product of 128 rows has at least 16 columns, so with
+// up to 8 heads the second part is free); that keeps 16 bits (bf16) or 22 (fp16) of a weight,
+// and they are scaled by 2^13 so that fp16 keeps those of a long tail (2^-38 of the largest).
+//
+// Work: the (sequence, key head, block of query heads, 128-key tile) units in that order, cut
+// into equal shares, one per persistent CTA, whatever the sequences' lengths.  A share's first
+// and last rows may be parts of longer ones: those partial results go to the workspace, and
+// paged_merge_kernel joins them in a fixed order (M = max lse, o = sum 2^(lse - M) o / sum).
+//
+// A CTA is six warps: four of softmax (warp w reads TMEM lanes 32 w ..: keys, or columns of O),
+// a TMA producer and an MMA issuer.  K and V tiles pass through one ring of 128-key x 128-column
+// slots (64 columns at d = 64) in the order K0 K1 V0 K2 V1 ...; QK runs a tile ahead of PV.
+// Pages of fewer than 128 slots make several TMA boxes per slot, one per producer lane.
 #include "attn_decode_paged.cuh"
+#include "attn_fwd_kernel.cuh"
 #include "ptx.cuh"
 #include "rope.cuh"
 #include "vec16.cuh"
@@ -9,111 +29,697 @@
 namespace gbattn {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 192;
+constexpr float kShift = 13.f;  // weights are kept times 2^13
+constexpr float kSlack = 2.f;   // the running maximum moves when a logit exceeds it by 2^2
 
-template <bool BF, int D>
-__global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedParams p) {
-  __shared__ float part[kWarps][D + 2];
-  grid_launch_dependents();
-  grid_wait_prior();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.x / p.Hq, h = blockIdx.x - b * p.Hq, hk = h / (p.Hq / p.Hkv);
-  constexpr int E = D / 32;  // elements 2 lane + 64 i + {0, 1} of a row
-  float q[E], acc[E], m = -INFINITY, l = 0.f;
-  const uint16_t *const qrow = static_cast<const uint16_t *>(p.q) + b * p.q_b + h * p.q_h;
-  auto load = [&](const uint16_t *row, float *x) {
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-      const uint32_t w = *reinterpret_cast<const uint32_t *>(row + 64 * i + 2 * lane);
-      if constexpr (BF) {
-        x[2 * i] = __uint_as_float(w << 16);
-        x[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
-      } else {
-        const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-        x[2 * i] = t.x;
-        x[2 * i + 1] = t.y;
+template <int D, int NH>
+struct PagedCfg {
+  static constexpr int CW = D == 64 ? 64 : 128;         // columns of a ring slot
+  static constexpr int NC = D / CW;                     // slots of a K or V tile
+  static constexpr int NBOX = CW / 64;                  // 64-column boxes of a slot
+  static constexpr int BOX_BYTES = kPagedTile * 128;
+  static constexpr int SLOT_BYTES = NBOX * BOX_BYTES;
+  static constexpr int NQ = NH < 16 ? 16 : NH;          // rows of the Q operand (a product of 128 rows has N % 16 = 0)
+  static constexpr int Q_BYTES = NQ * D * 2;
+  static constexpr int NP = 2 * NH;                     // columns of P^T: hi parts, then lo parts
+  static constexpr int P_BYTES = NP * kPagedTile * 2;
+  static constexpr int RED_BYTES = 3 * 4 * NH * 4;      // warps' maxima (two tiles) and sums
+  static constexpr int BAR_BYTES = 512;                 // barriers and a few words
+  static constexpr int ROOM = 232448 - 1024 - 2 * Q_BYTES - 2 * P_BYTES - RED_BYTES - BAR_BYTES;
+  static constexpr int FIT = ROOM / SLOT_BYTES, MOST = 196608 / SLOT_BYTES;
+  static constexpr int NSLOT = FIT < MOST ? FIT : MOST;
+  static_assert(NSLOT > NC, "a tile's V slots are resident together while the next K slots pass");
+  static constexpr int OFF_Q = NSLOT * SLOT_BYTES;
+  static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;
+  static constexpr int OFF_RED = OFF_P + 2 * P_BYTES;
+  static constexpr int OFF_BAR = OFF_RED + RED_BYTES;
+  // barriers
+  static constexpr int B_FULL = 0, B_EMPTY = NSLOT, B_QFULL = 2 * NSLOT, B_QEMPTY = B_QFULL + 2, B_SFULL = B_QEMPTY + 2,
+                       B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2, B_PDONE = B_PFULL + 2, B_DRAIN = B_PDONE + 2, NBAR = B_DRAIN + 1;
+  static constexpr int SMEM_BYTES = 1024 + OFF_BAR + BAR_BYTES;
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+  static constexpr int NO = D <= 128 ? 1 : D / 128;     // 128-column blocks of O
+  static constexpr int T_O = 2 * NQ;                    // TMEM columns: S twice, then O
+  static constexpr int T_USED = T_O + NO * NP;
+  static constexpr int T_COLS = T_USED <= 64 ? 64 : T_USED <= 128 ? 128 : T_USED <= 256 ? 256 : 512;
+  static_assert(T_USED <= 512, "tensor memory");
+};
+
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t (&r)[N]) {
+  if constexpr (N == 8) tmem_ld32x8(a, r);
+  else if constexpr (N == 16) tmem_ld32x16(a, r);
+  else if constexpr (N == 32) tmem_ld32x32(a, r);
+  else tmem_ld32x64(a, r);
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t (&r)[N]) {
+  if constexpr (N == 16) tmem_st32x16(a, r);
+  else if constexpr (N == 32) tmem_st32x32(a, r);
+  else tmem_st32x64(a, r);
+}
+
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// Tokens of sequence b, a bad length clamped into [0, table's end].
+__device__ __forceinline__ int clamp_length(int n, const PagedParams &p) {
+  const long long most = static_cast<long long>(p.table_w) * p.page;
+  return n < 0 ? 0 : n > most ? static_cast<int>(most) : n;
+}
+__device__ __forceinline__ int tiles_of(int n) { return (n >> 7) + ((n & 127) != 0); }
+
+// A run of one key head's (and block of query heads') tiles within a CTA's share.
+struct Seg {
+  int b, hv, len, tile, count, tiles;  // tiles: of the whole row
+};
+
+// Walks over a CTA's share, all lanes of a warp alike; 32 lengths are held at a time.
+struct Walk {
+  int b, hv, tile, hvs, base, held;
+  long long left;
+  const PagedParams &p;
+  __device__ Walk(const PagedParams &pp, int b0, long long off, long long n) : p(pp) {
+    hvs = pp.Hkv * pp.blocks;
+    b = b0;
+    left = n;
+    base = b0;
+    hv = tile = 0;
+    held = 0;
+    if (left > 0) {
+      fetch();
+      const int nt = tiles_of(length());
+      hv = static_cast<int>(off / nt);
+      tile = static_cast<int>(off - static_cast<long long>(hv) * nt);
+    }
+  }
+  __device__ void fetch() {
+    base = b;
+    const int i = b + static_cast<int>(threadIdx.x & 31);
+    held = i < p.B ? clamp_length(p.lengths[i], p) : 0;
+  }
+  __device__ int length() const { return __shfl_sync(0xffffffffu, held, b - base); }
+  __device__ bool next(Seg &s) {
+    if (left <= 0) return false;
+    s.b = b;
+    s.hv = hv;
+    s.len = length();
+    s.tile = tile;
+    s.tiles = tiles_of(s.len);
+    s.count = static_cast<int>(min(left, static_cast<long long>(s.tiles - tile)));
+    left -= s.count;
+    tile += s.count;
+    if (tile == s.tiles) {
+      tile = 0;
+      if (++hv == hvs) {
+        hv = 0;
+        do {
+          if (++b - base == 32 && b < p.B) fetch();
+        } while (left > 0 && b < p.B && length() == 0);
       }
     }
-  };
-  load(qrow, q);
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  long long n = p.lengths[b];
-  const long long most = static_cast<long long>(p.table_w) * p.page;
-  if (n < 0 || n > most) {
-    if (threadIdx.x == 0) atomicCAS(p.status, 0u, kDevBadLength);
-    n = n < 0 ? 0 : most;
+    return true;
   }
-  for (long long j = warp; j < n; j += kWarps) {
-    const int page = p.table[b * p.table_s + j / p.page];
-    float k[E], v[E];
-    if (page < 0 || page >= p.pages) {
-      if (lane == 0) atomicCAS(p.status, 0u, kDevBadPage);
-#pragma unroll
-      for (int e = 0; e < E; ++e) k[e] = v[e] = 0.f;
-    } else {
-      const long long at = page * p.page_s + hk * p.head_s + (j % p.page) * p.slot_s;
-      load(static_cast<const uint16_t *>(p.k_pages) + at, k);
-      load(static_cast<const uint16_t *>(p.v_pages) + at, v);
+};
+
+// The same, tile by tile.
+struct Tile {
+  int b, hv, n, pos;  // valid keys in the tile; its first position
+  int seg;            // number of its segment within the share
+  bool first, last;   // of its segment
+};
+struct Tiles {
+  Walk w;
+  Seg s;
+  int i = 0, seg = -1;
+  __device__ Tiles(const Walk &walk) : w(walk) { s.count = 0; }
+  __device__ bool next(Tile &t) {
+    if (i == s.count) {
+      if (!w.next(s)) return false;
+      i = 0;
+      ++seg;
     }
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], k[e], s);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    s *= p.c2;
-    const float top = fmaxf(m, s);
-    const float base = top == -INFINITY ? 0.f : top;
-    const float keep = ex2_approx(m - base), w = ex2_approx(s - base);
-    m = top;
-    l = l * keep + w;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * keep + w * v[e];
+    t.b = s.b;
+    t.hv = s.hv;
+    t.pos = (s.tile + i) * kPagedTile;
+    t.n = min(kPagedTile, s.len - t.pos);
+    t.seg = seg;
+    t.first = i == 0;
+    t.last = ++i == s.count;
+    return true;
   }
-#pragma unroll
-  for (int i = 0; i < E / 2; ++i) {
-    part[warp][64 * i + 2 * lane] = acc[2 * i];
-    part[warp][64 * i + 2 * lane + 1] = acc[2 * i + 1];
+};
+
+// Where a tile's V begins in the ring's order K0 K1 V0 K2 V1 ... (T tiles, nc slots each).
+__device__ __forceinline__ long long v_pos(long long t, long long T, int nc) { return (min(t + 2, T) + t) * nc; }
+
+template <int D, int NH>
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
+  using C = PagedCfg<D, NH>;
+  extern __shared__ uint8_t smem_raw[];
+  struct Misc {
+    long long warp_tiles[kThreads / 32], start_off;
+    int start_b;
+    uint32_t tmem_base;
+    volatile uint32_t abort_flag;
+  };
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *const base_ptr = smem_raw + (base - raw);
+  float *const red = reinterpret_cast<float *>(base_ptr + C::OFF_RED);
+  Misc &misc = *reinterpret_cast<Misc *>(base_ptr + C::OFF_BAR + 8 * C::NBAR);
+  static_assert(8 * C::NBAR + sizeof(Misc) <= C::BAR_BYTES, "barrier room");
+  const uint32_t bars = base + C::OFF_BAR;
+  auto BAR = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < C::NSLOT; ++i) {
+      mbar_init(BAR(C::B_FULL + i), 1);
+      mbar_init(BAR(C::B_EMPTY + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(BAR(C::B_QFULL + i), 1);
+      mbar_init(BAR(C::B_QEMPTY + i), 1);
+      mbar_init(BAR(C::B_SFULL + i), 1);
+      mbar_init(BAR(C::B_SFREE + i), 4);
+      mbar_init(BAR(C::B_PFULL + i), 4);
+      mbar_init(BAR(C::B_PDONE + i), 1);
+    }
+    mbar_init(BAR(C::B_DRAIN), 1);
+    misc.abort_flag = 0u;
+    misc.start_b = 0;
+    misc.start_off = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
   }
-  if (lane == 0) {
-    part[warp][D] = m;
-    part[warp][D + 1] = l;
+  if (warp == 4) {
+    tmem_alloc(smem_u32(&misc.tmem_base), C::T_COLS);
+    tmem_relinquish();
+  }
+  grid_launch_dependents();
+  grid_wait_prior();  // what follows reads the previous kernels' results
+
+  // ------------------------------------------------------------ this CTA's share
+  // Thread i counts the units of its run of sequences; a scan over the block gives the total
+  // and finds the sequence in which this CTA's share begins.
+  const int hvs = p.Hkv * p.blocks;
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int s0 = min(p.B, tid * per), s1 = min(p.B, s0 + per);
+  long long mine = 0;
+  for (int b = s0; b < s1; ++b) {
+    const int n = p.lengths[b], m = clamp_length(n, p);
+    if (n != m && blockIdx.x == 0) atomicCAS(p.status, 0u, kDevBadLength);
+    mine += static_cast<long long>(tiles_of(m)) * hvs;
+  }
+  long long upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) misc.warp_tiles[warp] = upto;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) upto += misc.warp_tiles[w];
+    total += misc.warp_tiles[w];
+  }
+  // The first G CTAs have a unit at least, the others none: a row's parts lie in CTAs next to one another.
+  const long long G = min(static_cast<long long>(gridDim.x), max(total, 1LL)), cta = min(static_cast<long long>(blockIdx.x), G);
+  const long long u0 = total * cta / G, u1 = total * min(cta + 1, G) / G;
+  if (u0 < u1 && upto - mine <= u0 && u0 < upto) {
+    long long off = u0 - (upto - mine);
+    for (int b = s0; b < s1; ++b) {
+      const long long units = static_cast<long long>(tiles_of(clamp_length(p.lengths[b], p))) * hvs;
+      if (off < units) {
+        misc.start_b = b;
+        misc.start_off = off;
+        break;
+      }
+      off -= units;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc.tmem_base;
+  const long long T = u1 - u0;
+  const Walk walk(p, misc.start_b, misc.start_off, T);
+  bool ok = true;
+
+  if (warp == 4) {
+    // ---------------------------------------------------------- producer
+    Tiles it(walk);
+    const int rows = p.box_rows, chunks = kPagedTile / rows, lanes = chunks * C::NBOX;
+    const int row = (lane / C::NBOX) * rows, box = lane % C::NBOX;  // this lane's box of a slot
+    long long at = 0;  // slots filled
+    int queries = 0;   // query tiles loaded
+    struct Load {
+      Tile t;
+      int page, slot;
+    };
+    auto look = [&](Load &l) -> bool {  // the next tile, and this lane's page of it
+      if (!it.next(l.t)) return false;
+      l.page = l.slot = 0;
+      if (row < l.t.n && lane < lanes) {
+        const int pos = l.t.pos + row, index = pos / p.page;
+        l.slot = pos - index * p.page;
+        l.page = p.table[l.t.b * p.table_s + index];
+      }
+      return true;
+    };
+    auto fill = [&](const Load &l, const CUtensorMap *tm) {
+      if (l.page < 0 || l.page >= p.pages) atomicCAS(p.status, 0u, kDevBadPage);  // TMA reads zeros there
+      const uint32_t bytes = static_cast<uint32_t>((l.t.n + rows - 1) / rows * rows) * 128u * C::NBOX;
+      const int head = l.t.hv / p.blocks;
+      for (int c = 0; ok && c < C::NC; ++c, ++at) {
+        const uint32_t slot = static_cast<uint32_t>(at % C::NSLOT);
+        if (at >= C::NSLOT)
+          ok = __all_sync(0xffffffffu, wait_bounded(BAR(C::B_EMPTY + slot), (at / C::NSLOT - 1) & 1, &misc.abort_flag, p.status,
+                                                    kDevTimeoutLoad, p.wait_limit));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(BAR(C::B_FULL + slot), bytes);
+        __syncwarp();
+        if (lane < lanes && row < l.t.n)
+          tma_load_4d(base + slot * C::SLOT_BYTES + box * C::BOX_BYTES + row * 128, tm, c * C::CW + box * 64, l.slot, head, l.page,
+                      BAR(C::B_FULL + slot));
+      }
+    };
+    auto query = [&](const Tile &t) {  // Q of a segment, before its first K
+      const int s = t.seg;
+      if (s >= 2)
+        ok = __all_sync(0xffffffffu, wait_bounded(BAR(C::B_QEMPTY + (s & 1)), ((s - 2) >> 1) & 1, &misc.abort_flag, p.status,
+                                                  kDevTimeoutLoad, p.wait_limit));
+      if (!ok || lane != 0) return;
+      queries = s + 1;
+      const uint32_t bar = BAR(C::B_QFULL + (s & 1)), dst = base + C::OFF_Q + (s & 1) * C::Q_BYTES;
+      mbar_arrive_expect_tx(bar, static_cast<uint32_t>(p.q_rows) * 128u * (D / 64));
+      const int head = (t.hv / p.blocks) * p.G + (t.hv % p.blocks) * NH;
+      for (int x = 0; x < D / 64; ++x) tma_load_3d(dst + x * C::NQ * 128, &tm_q, x * 64, head, t.b, bar);
+    };
+    Load v, k, ahead;
+    bool have_v = false, have_k = look(k);
+    while (ok && (have_k || have_v)) {
+      const bool have_a = have_k && look(ahead);
+      if (have_k) {
+        if (k.t.first) query(k.t);
+        if (ok) fill(k, &tm_k);
+      }
+      if (ok && have_v) fill(v, &tm_v);
+      v = k;
+      have_v = have_k;
+      k = ahead;
+      have_k = have_a;
+    }
+    // After a time-out: copies that nobody waited for land before the CTA ends.
+    if (lane == 0 && misc.abort_flag) {
+      for (long long x = max(0LL, at - C::NSLOT); x < at; ++x)
+        wait_drain(BAR(C::B_FULL + static_cast<int>(x % C::NSLOT)), (x / C::NSLOT) & 1, p.wait_limit);
+      for (int x = max(0, queries - 2); x < queries; ++x) wait_drain(BAR(C::B_QFULL + (x & 1)), (x >> 1) & 1, p.wait_limit);
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    // ---------------------------------------------------------- MMA issuer
+    const uint32_t idesc_s = p.bf16 ? idesc_bf16_f32(128, C::NQ, 0, 0) : idesc_f16_f32(128, C::NQ, 0, 0);
+    const uint32_t idesc_o = p.bf16 ? idesc_bf16_f32(128, C::NP, 1, 0) : idesc_f16_f32(128, C::NP, 1, 0);
+    const SDesc dk = sdesc_split(sdesc_sw128(base, 16, 1024));
+    // V^T: 64-column boxes BOX_BYTES apart; at d = 64 there is one, read twice (rows 64 .. of O are not used)
+    const SDesc dv = sdesc_split(sdesc_sw128(base, C::NBOX == 1 ? 0 : C::BOX_BYTES, 1024));
+    const SDesc dq = sdesc_split(sdesc_sw128(base + C::OFF_Q, 16, 1024));
+    const SDesc dp = sdesc_split(sdesc_sw128(base + C::OFF_P, 16, 1024));
+    auto wait = [&](int bar, long long phase) {
+      ok = ok && __all_sync(0xffffffffu, wait_bounded(BAR(bar), static_cast<uint32_t>(phase & 1), &misc.abort_flag, p.status, kDevTimeoutMma,
+                                                      p.wait_limit));
+    };
+    long long at = 0;
+    Tiles it(walk);
+    Tile cur, nxt;
+    auto qk = [&](const Tile &t, long long i) {
+      const int buf = static_cast<int>(i & 1), qb = t.seg & 1;
+      if (t.first) wait(C::B_QFULL + qb, t.seg >> 1);
+      if (i >= 2) wait(C::B_SFREE + buf, (i - 2) >> 1);
+      for (int c = 0; ok && c < C::NC; ++c, ++at) {
+        const uint32_t slot = static_cast<uint32_t>(at % C::NSLOT);
+        wait(C::B_FULL + slot, at / C::NSLOT);
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int kk = 0; kk < C::CW / 16; ++kk)
+            umma_ss_off(tmem + buf * C::NQ, dk, slot * C::SLOT_BYTES + (kk >> 2) * C::BOX_BYTES + (kk & 3) * 32, dq,
+                        qb * C::Q_BYTES + (c * C::NBOX + (kk >> 2)) * C::NQ * 128 + (kk & 3) * 32, idesc_s, (c | kk) != 0);
+          umma_commit(BAR(C::B_EMPTY + slot));
+        }
+        __syncwarp();
+      }
+      if (ok && lane == 0) {
+        umma_commit(BAR(C::B_SFULL + buf));
+        if (t.last) umma_commit(BAR(C::B_QEMPTY + qb));
+      }
+      __syncwarp();
+    };
+    auto pv = [&](const Tile &t, long long i) {
+      const int buf = static_cast<int>(i & 1);
+      wait(C::B_PFULL + buf, i >> 1);
+      for (int c = 0; ok && c < C::NC; ++c, ++at) {
+        const uint32_t slot = static_cast<uint32_t>(at % C::NSLOT);
+        wait(C::B_FULL + slot, at / C::NSLOT);
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int kk = 0; kk < kPagedTile / 16; ++kk)
+            umma_ss_off(tmem + C::T_O + c * C::NP, dv, slot * C::SLOT_BYTES + kk * 2048, dp,
+                        buf * C::P_BYTES + (kk >> 2) * C::NP * 128 + (kk & 3) * 32, idesc_o, !t.first || kk > 0);
+          umma_commit(BAR(C::B_EMPTY + slot));
+        }
+        __syncwarp();
+      }
+      if (ok && lane == 0) umma_commit(BAR(C::B_PDONE + buf));
+      __syncwarp();
+    };
+    bool have = it.next(cur);
+    if (have) qk(cur, 0);
+    for (long long i = 0; ok && have; ++i) {
+      have = it.next(nxt);
+      if (have) qk(nxt, i + 1);
+      if (ok) pv(cur, i);
+      cur = nxt;
+    }
+    if (misc.abort_flag && lane == 0) {  // after a time-out: products in flight end before the CTA does
+      umma_commit(BAR(C::B_DRAIN));
+      wait_drain(BAR(C::B_DRAIN), 0, p.wait_limit);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------- softmax (and empty sequences)
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp) << 21);  // this warp's 32 TMEM lanes
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+      if (clamp_length(p.lengths[b], p) == 0) {
+        uint32_t *const o = static_cast<uint32_t *>(p.o) + static_cast<size_t>(b) * p.Hq * (D / 2);
+        for (int i = tid; i < p.Hq * (D / 2); i += 128) o[i] = 0u;
+        for (int i = tid; i < p.Hq; i += 128) p.lse[static_cast<size_t>(b) * p.Hq + i] = -INFINITY;
+      }
+    PagedRecord record = {0, 0, 0, 0};
+    auto wait = [&](int bar, long long phase) {
+      ok = __all_sync(0xffffffffu, wait_bounded(BAR(bar), static_cast<uint32_t>(phase & 1), &misc.abort_flag, p.status, kDevTimeoutSoftmax,
+                                                p.wait_limit)) && ok;
+    };
+    Walk w(walk);
+    Seg s;
+    long long i = 0;  // tiles done
+    while (w.next(s)) {
+      const int block = s.hv % p.blocks, heads = min(NH, p.G - block * NH);
+      float m[NH], l[NH];
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        m[h] = -INFINITY;
+        l[h] = 0.f;
+      }
+      for (int j = 0; j < s.count; ++j, ++i) {
+        // After a time-out the remaining tiles run through the barriers only.
+        const int buf = static_cast<int>(i & 1), n = s.len - (s.tile + j) * kPagedTile;
+        uint32_t x[NH];
+        wait(C::B_SFULL + buf, i >> 1);
+        tc_fence_after();
+        tmem_ld<NH>(lanes + buf * C::NQ, x);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(C::B_SFREE + buf));
+        float top[NH];
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+          if (h < heads) {
+            const float v = tid < n ? __uint_as_float(x[h]) * p.c2 : -INFINITY;
+            x[h] = __float_as_uint(v);
+            top[h] = warp_max(v);
+          } else {
+            top[h] = 0.f;
+          }
+        float *const mine_r = red + (buf * 4 + warp) * NH;
+        if (lane == 0) {
+#pragma unroll
+          for (int h = 0; h < NH; h += 4) *reinterpret_cast<float4 *>(mine_r + h) = make_float4(top[h], top[h + 1], top[h + 2], top[h + 3]);
+        }
+        softmax_sync();
+        // ---- the running maximum, and what it does to the sums and to O
+        bool moved = false;
+        float keep[NH];
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          keep[h] = 1.f;
+          if (h < heads) {
+            const float *const r = red + buf * 4 * NH + h;
+            const float t = fmaxf(fmaxf(r[0], r[NH]), fmaxf(r[2 * NH], r[3 * NH]));
+            if (j == 0 || t > m[h] + kSlack) {
+              if (j > 0) {
+                keep[h] = ex2_approx(m[h] - t);
+                l[h] *= keep[h];
+                moved = true;
+              }
+              m[h] = t;
+            }
+          }
+        }
+        // ---- the weights of this thread's key, as hi + lo
+        if (i >= 2) wait(C::B_PDONE + buf, (i - 2) >> 1);
+        const uint32_t prow = base + C::OFF_P + buf * C::P_BYTES + (tid >> 6) * (C::NP * 128) + (tid & 7) * 2;
+        const uint32_t pcol = (tid & 63) >> 3;
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+          if (h < heads) {
+            const float e = ex2_approx(__uint_as_float(x[h]) - (m[h] == -INFINITY ? 0.f : m[h] - kShift));
+            l[h] += e;
+            uint32_t parts;
+            if (p.bf16) {
+              const __nv_bfloat16 hi = __float2bfloat16_rn(e);
+              const __nv_bfloat16 lo = __float2bfloat16_rn(e - __bfloat162float(hi));
+              parts = __bfloat16_as_ushort(hi) | (static_cast<uint32_t>(__bfloat16_as_ushort(lo)) << 16);
+            } else {
+              const __half hi = __float2half_rn(e);
+              const __half lo = __float2half_rn(e - __half2float(hi));
+              parts = __half_as_ushort(hi) | (static_cast<uint32_t>(__half_as_ushort(lo)) << 16);
+            }
+            const uint32_t a = prow + h * 128 + ((pcol ^ (h & 7)) << 4);  // row NH + h has the same swizzle (NH % 8 = 0)
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"(static_cast<uint16_t>(parts)) : "memory");
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(a + NH * 128), "h"(static_cast<uint16_t>(parts >> 16)) : "memory");
+          }
+        if (moved) {  // the same in every thread
+          wait(C::B_PDONE + (buf ^ 1), (i - 1) >> 1);
+          if (ok) {
+            tc_fence_after();
+#pragma unroll
+            for (int ob = 0; ob < C::NO; ++ob) {
+              uint32_t o[C::NP];
+              tmem_ld<C::NP>(lanes + C::T_O + ob * C::NP, o);
+#pragma unroll
+              for (int h = 0; h < NH; ++h) {
+                o[h] = __float_as_uint(__uint_as_float(o[h]) * keep[h]);
+                o[NH + h] = __float_as_uint(__uint_as_float(o[NH + h]) * keep[h]);
+              }
+              tmem_st<C::NP>(lanes + C::T_O + ob * C::NP, o);
+            }
+          }
+        }
+        if (n < kPagedTile) {
+          // Whatever lies behind the last token (unwritten slots, earlier tiles) times a weight of
+          // zero must be zero: clear those rows of V.
+          const long long v0 = v_pos(i, T, C::NC);
+          for (int c = 0; c < C::NC; ++c) {
+            const uint32_t slot = static_cast<uint32_t>((v0 + c) % C::NSLOT);
+            wait(C::B_FULL + slot, (v0 + c) / C::NSLOT);
+            if (ok && tid >= n)
+#pragma unroll
+              for (int z = 0; z < C::NBOX * 8; ++z)
+                st_shared_v4(base + slot * C::SLOT_BYTES + (z >> 3) * C::BOX_BYTES + tid * 128 + (z & 7) * 16, 0, 0, 0, 0);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(C::B_PFULL + buf));
+      }
+      // ---------------------------------------------------------- the segment's results
+      float *const sums = red + 8 * NH;
+#pragma unroll
+      for (int h = 0; h < NH; ++h)
+        if (h < heads) {
+          float t = l[h];
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+          if (lane == 0) sums[warp * NH + h] = t;
+        }
+      softmax_sync();
+      wait(C::B_PDONE + static_cast<int>((i - 1) & 1), (i - 1) >> 1);
+      tc_fence_after();
+      const bool whole = s.count == s.tiles, begins = s.tile == 0;
+      const int head0 = (s.hv / p.blocks) * p.G + block * NH;
+      const size_t row0 = static_cast<size_t>(s.b) * p.Hq + head0;
+      const size_t part = 2 * static_cast<size_t>(blockIdx.x) + (begins ? 1 : 0);
+      float inv[NH];
+#pragma unroll
+      for (int h = 0; h < NH; ++h)
+        if (h < heads) {
+          const float t = sums[h] + sums[NH + h] + (sums[2 * NH + h] + sums[3 * NH + h]);
+          inv[h] = t == 0.f ? 0.f : 1.f / t;
+          if (ok && tid == h) {
+            const float lse2 = m[h] - kShift + __log2f(t);
+            if (whole)
+              p.lse[row0 + h] = lse2 * 0.69314718055994531f;
+            else
+              p.part_lse[part * NH + h] = lse2;
+          }
+        }
+#pragma unroll
+      for (int ob = 0; ob < C::NO; ++ob) {
+        uint32_t o[C::NP];
+        tmem_ld<C::NP>(lanes + C::T_O + ob * C::NP, o);
+        const int col = ob * 128 + tid;
+        if (ok && (D >= 128 || tid < D))
+#pragma unroll
+          for (int h = 0; h < NH; ++h)
+            if (h < heads) {
+              const float y = (__uint_as_float(o[h]) + __uint_as_float(o[NH + h])) * inv[h];
+              if (!whole)
+                p.part_o[(part * NH + h) * D + col] = y;
+              else if (p.bf16)
+                static_cast<__nv_bfloat16 *>(p.o)[(row0 + h) * D + col] = __float2bfloat16_rn(y);
+              else
+                static_cast<__half *>(p.o)[(row0 + h) * D + col] = __float2half_rn(y);
+            }
+      }
+      tc_fence_before();
+      if (!whole && begins) {
+        // The row goes on in the next CTAs: up to the one whose share holds its last unit.
+        const long long end = u1 + (s.tiles - s.count) - 1;
+        long long c = end * G / total;
+        while (total * (c + 1) / G <= end) ++c;
+        while (total * c / G > end) --c;
+        record.head = static_cast<int>(row0);
+        record.heads = heads;
+        record.parts = static_cast<int>(c) - static_cast<int>(blockIdx.x) + 1;
+      }
+    }
+    if (tid == 0 && p.records) p.records[blockIdx.x] = record;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) tmem_dealloc(tmem, C::T_COLS);
+}
+
+// Joins the rows that were cut: block (c, h) the h-th head of the row that CTA c's share ends in.
+template <int D, int NH>
+__global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
+  __shared__ float weight[kPagedMaxCtas];
+  __shared__ float shared_sum;
+  grid_launch_dependents();
+  grid_wait_prior();
+  const PagedRecord r = p.records[blockIdx.x];
+  const int h = blockIdx.y, tid = threadIdx.x;
+  if (h >= r.heads) return;
+  auto part = [&](int i) -> size_t { return i == 0 ? 2 * static_cast<size_t>(blockIdx.x) + 1 : 2 * (static_cast<size_t>(blockIdx.x) + i); };
+  for (int i = tid; i < r.parts; i += 128) weight[i] = p.part_lse[part(i) * NH + h];
+  __syncthreads();
+  if (tid < 32) {
+    float M = -INFINITY, sum = 0.f;
+    bool nan = false;
+    for (int i = tid; i < r.parts; i += 32) {
+      M = fmaxf(M, weight[i]);
+      nan = nan || weight[i] != weight[i];
+    }
+    M = warp_max(M);
+    const float from = M == -INFINITY ? 0.f : M;
+    for (int i = tid; i < r.parts; i += 32) {
+      const float w = ex2_approx(weight[i] - from);
+      weight[i] = w;
+      sum += w;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (__any_sync(0xffffffffu, nan)) sum = NAN;
+    if (tid == 0) {
+      shared_sum = sum;
+      p.lse[r.head + h] = (M + __log2f(sum)) * 0.69314718055994531f;
+    }
   }
   __syncthreads();
-  float top = -INFINITY, sum = 0.f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part[w][D]);
-  const float base = top == -INFINITY ? 0.f : top;
-  for (int w = 0; w < kWarps; ++w) sum += part[w][D + 1] * ex2_approx(part[w][D] - base);
-  for (int c = threadIdx.x; c < D; c += kThreads) {
+  const float sum = shared_sum, inv = sum == 0.f ? 0.f : 1.f / sum;
+  for (int c = tid; c < D; c += 128) {
     float o = 0.f;
-    for (int w = 0; w < kWarps; ++w) o += part[w][c] * ex2_approx(part[w][D] - base);
-    o = sum > 0.f ? o / sum : (sum == 0.f ? 0.f : sum);
-    const size_t at = static_cast<size_t>(blockIdx.x) * D + c;
-    if constexpr (BF)
+#pragma unroll 8
+    for (int i = 0; i < r.parts; ++i) o = fmaf(weight[i], p.part_o[(part(i) * NH + h) * D + c], o);
+    o *= inv;
+    const size_t at = static_cast<size_t>(r.head + h) * D + c;
+    if (p.bf16)
       static_cast<__nv_bfloat16 *>(p.o)[at] = __float2bfloat16_rn(o);
     else
       static_cast<__half *>(p.o)[at] = __float2half_rn(o);
   }
-  if (threadIdx.x == 0) p.lse[blockIdx.x] = (top + log2f(sum)) * 0.69314718055994531f;
 }
 
-}  // namespace
-
-cudaError_t launch_decode_paged(const PagedLaunch &a) {
+template <int D, int NH>
+cudaError_t launch_paged(const PagedLaunch &a) {
+  using C = PagedCfg<D, NH>;
+  auto *kern = decode_paged_kernel<D, NH>;
+  static unsigned long long configured = 0;  // a bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(configured >> dev & 1)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) configured |= 1ull << dev;
+  }
+  // At most one CTA per unit of work that the tables have room for.
+  const long long row_tiles = (static_cast<long long>(a.p.table_w) * a.p.page + kPagedTile - 1) / kPagedTile;
+  const long long units = static_cast<long long>(a.p.B) * a.p.Hkv * a.p.blocks * row_tiles;
+  const unsigned grid = static_cast<unsigned>(std::min<long long>(units, std::min(a.sm_count, kPagedMaxCtas)));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.p.B) * static_cast<unsigned>(a.p.Hq));
+  cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
   cfg.stream = a.stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  PagedParams p = a.p;
+  const bool cut = row_tiles > 1;  // a row of one tile is never cut
+  if (!cut) p.records = nullptr;
+  e = cudaLaunchKernelEx(&cfg, kern, a.tm_q, a.tm_k, a.tm_v, p);
+  if (e != cudaSuccess || !cut) return e;
+  cfg.gridDim = dim3(grid, static_cast<unsigned>(std::min(NH, a.p.G)));
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, NH>, p);
+}
+
+template <int D>
+cudaError_t launch_paged_d(const PagedLaunch &a) {
+  switch (paged_heads(a.p.G, D)) {
+    case 8: return launch_paged<D, 8>(a);
+    case 16: return launch_paged<D, 16>(a);
+    default:
+      if constexpr (D <= 256) return launch_paged<D, 32>(a);
+      return cudaErrorInvalidValue;  // paged_heads gives at most 16 there
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_decode_paged(const PagedLaunch &a) {
   switch (a.p.d) {
-    case 64: return cudaLaunchKernelEx(&cfg, a.bf16 ? decode_paged_kernel<true, 64> : decode_paged_kernel<false, 64>, a.p);
-    case 128: return cudaLaunchKernelEx(&cfg, a.bf16 ? decode_paged_kernel<true, 128> : decode_paged_kernel<false, 128>, a.p);
-    case 256: return cudaLaunchKernelEx(&cfg, a.bf16 ? decode_paged_kernel<true, 256> : decode_paged_kernel<false, 256>, a.p);
-    default: return cudaLaunchKernelEx(&cfg, a.bf16 ? decode_paged_kernel<true, 512> : decode_paged_kernel<false, 512>, a.p);
+    case 64: return launch_paged_d<64>(a);
+    case 128: return launch_paged_d<128>(a);
+    case 256: return launch_paged_d<256>(a);
+    default: return launch_paged_d<512>(a);
   }
 }
 

@@ -10,26 +10,51 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 namespace gbattn {
 
+constexpr int kPagedMaxCtas = 152;  // persistent CTAs at most (one per SM); sizes the workspace
+constexpr int kPagedTile = 128;     // keys per tile
+
+// Query heads of one key head that a CTA works on at once, and how many such blocks of heads
+// a key head's G query heads make (each reads the keys again).
+constexpr int paged_heads(int G, int d) { return G <= 8 ? 8 : G <= 16 || d > 256 ? 16 : 32; }
+constexpr int paged_blocks(int G, int d) { return (G + paged_heads(G, d) - 1) / paged_heads(G, d); }
+
+// Workspace: a record per CTA, then two partial results per CTA, each of paged_heads rows of
+// o[d] (normalised), then the base-2 log-sum-exps of all rows.
+struct PagedRecord {
+  int head;   // b * Hq + first query head of the rows that this CTA's last partial begins; unused when parts = 0
+  int heads;
+  int parts;  // partial results to join: this CTA's second, then the first of each of the following parts - 1 CTAs
+  int pad;
+};
+constexpr long long paged_workspace_bytes(int G, int d) {
+  return kPagedMaxCtas * (16LL + 2LL * paged_heads(G, d) * (d + 1) * 4);
+}
+
 struct PagedParams {
-  const void *q;                       // [B, Hq, d] by strides
-  long long q_b, q_h;
-  const void *k_pages, *v_pages;       // [pages, Hkv, page, d] by strides
-  long long page_s, head_s, slot_s;
+  PagedRecord *records;                // workspace
+  float *part_o, *part_lse;            // [2 kPagedMaxCtas][heads][d], [2 kPagedMaxCtas][heads]
   const int *table, *lengths;
   long long table_s;
   int table_w, page, pages;
   int B, Hq, Hkv, d;
+  int G, blocks;                       // query heads per key head; blocks of them
+  int box_rows;                        // rows of a TMA box: a power of two <= 128 that divides the page
+  int q_rows;                          // rows of a query box
+  bool bf16;
   float c2;                            // scale log2(e)
   void *o;                             // [B, Hq, d]
   float *lse;                          // [B, Hq]
   unsigned *status;
+  long long wait_limit;
 };
 
 struct PagedLaunch {
+  CUtensorMap tm_q, tm_k, tm_v;
   PagedParams p;
-  bool bf16;
   int sm_count;
   cudaStream_t stream;
 };

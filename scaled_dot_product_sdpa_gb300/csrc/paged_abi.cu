@@ -3,6 +3,7 @@
 // attn_cache_append, attn_cache_copy and attn_decode_paged.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdlib>
@@ -370,7 +371,7 @@ extern "C" long long attn_decode_paged_workspace_bytes(int Hq, int Hkv, int d) {
   if (Hq <= 0 || Hkv <= 0) return GBATTN_ERR_DIMS;
   if (Hq % Hkv) return GBATTN_ERR_HEADS;
   if (!head_dim_ok(d)) return GBATTN_ERR_HEAD_DIM;
-  return 16;
+  return paged_workspace_bytes(Hq / Hkv, d);
 }
 
 extern "C" int attn_decode_paged(const void *q, long long q_sb, long long q_sh, const void *k_pages, const void *v_pages,
@@ -399,30 +400,45 @@ extern "C" int attn_decode_paged(const void *q, long long q_sb, long long q_sh, 
                       pages_span(v_pages, page_stride, extent, pages),
                       dense_span(table, (B - 1LL) * table_stride + table_width, 4), dense_span(lengths, B, 4)};
   if (!disjoint(out, 3, in, 5)) return GBATTN_ERR_ALIAS;
-  PagedLaunch a = {};
-  if ((rc = abi_device(&a.sm_count, &a.p.status)) != GBATTN_OK) return rc;
-  a.p.q = q;
-  a.p.q_b = q_sb;
-  a.p.q_h = q_sh;
-  a.p.k_pages = k_pages;
-  a.p.v_pages = v_pages;
-  a.p.page_s = page_stride;
-  a.p.head_s = head_stride;
-  a.p.slot_s = slot_stride;
-  a.p.table = table;
-  a.p.table_s = table_stride;
-  a.p.table_w = table_width;
-  a.p.lengths = lengths;
-  a.p.page = page;
-  a.p.pages = pages;
-  a.p.B = B;
-  a.p.Hq = Hq;
-  a.p.Hkv = Hkv;
-  a.p.d = d;
-  a.p.c2 = scale * 1.4426950408889634f;
-  a.p.o = o;
-  a.p.lse = lse;
-  a.bf16 = dtype == GBATTN_BF16;
+  PagedLaunch a;
+  PagedParams &p = a.p;
+  p = {};
+  if ((rc = abi_device(&a.sm_count, &p.status)) != GBATTN_OK) return rc;
+  p.table = table;
+  p.table_s = table_stride;
+  p.table_w = table_width;
+  p.lengths = lengths;
+  p.page = page;
+  p.pages = pages;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.d = d;
+  p.G = Hq / Hkv;
+  p.blocks = paged_blocks(p.G, d);
+  p.box_rows = std::min(page & -page, kPagedTile);
+  const int rows_at_once = paged_heads(p.G, d);
+  p.q_rows = std::min(rows_at_once, p.G);
+  p.bf16 = dtype == GBATTN_BF16;
+  p.c2 = scale * 1.4426950408889634f;
+  p.o = o;
+  p.lse = lse;
+  p.wait_limit = 1LL << 32;  // about two seconds of SM clock
+  p.records = static_cast<PagedRecord *>(workspace);
+  p.part_o = reinterpret_cast<float *>(p.records + kPagedMaxCtas);
+  p.part_lse = p.part_o + 2LL * kPagedMaxCtas * rows_at_once * d;
+  // [pages, Hkv, page, d] by strides; a dimension of one element may have any stride
+  auto bytes = [](long long stride, long long count, int d) { return static_cast<cuuint64_t>(count > 1 ? stride : d) * 2u; };
+  const cuuint64_t kv_dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page), static_cast<cuuint64_t>(Hkv),
+                                 static_cast<cuuint64_t>(pages)};
+  const cuuint64_t kv_strides[3] = {bytes(slot_stride, page, d), bytes(head_stride, Hkv, d), bytes(page_stride, pages, d)};
+  const cuuint32_t kv_box[4] = {64, static_cast<cuuint32_t>(p.box_rows), 1, 1};
+  const cuuint64_t q_dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(Hq), static_cast<cuuint64_t>(B)};
+  const cuuint64_t q_strides[2] = {bytes(q_sh, Hq, d), bytes(q_sb, B, d)};
+  const cuuint32_t q_box[3] = {64, static_cast<cuuint32_t>(p.q_rows), 1};
+  if (abi_encode(&a.tm_q, p.bf16, 3, q, q_dims, q_strides, q_box) || abi_encode(&a.tm_k, p.bf16, 4, k_pages, kv_dims, kv_strides, kv_box) ||
+      abi_encode(&a.tm_v, p.bf16, 4, v_pages, kv_dims, kv_strides, kv_box))
+    return GBATTN_ERR_TENSORMAP;
   a.stream = static_cast<cudaStream_t>(stream);
   return done(launch_decode_paged(a));
 }
