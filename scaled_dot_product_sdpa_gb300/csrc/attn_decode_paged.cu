@@ -29,7 +29,9 @@
 namespace gbattn {
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kProducers = 3;  // producer warps
+constexpr int kAhead = 4;      // tiles whose page numbers a producer reads ahead
+constexpr int kThreads = 160 + 32 * kProducers;
 constexpr float kShift = 13.f;  // weights are kept times 2^13
 constexpr float kSlack = 2.f;   // the running maximum moves when a logit exceeds it by 2^2
 
@@ -45,15 +47,17 @@ struct PagedCfg {
   static constexpr int NP = 2 * NH;                     // columns of P^T: hi parts, then lo parts
   static constexpr int P_BYTES = NP * kPagedTile * 2;
   static constexpr int RED_BYTES = 3 * 4 * NH * 4;      // warps' maxima (two tiles) and sums
+  static constexpr int PAGE_BYTES = kProducers * kAhead * 32 * 4;  // page numbers read ahead, per producer lane
   static constexpr int BAR_BYTES = 512;                 // barriers and a few words
-  static constexpr int ROOM = 232448 - 1024 - 2 * Q_BYTES - 2 * P_BYTES - RED_BYTES - BAR_BYTES;
+  static constexpr int ROOM = 232448 - 1024 - 2 * Q_BYTES - 2 * P_BYTES - RED_BYTES - PAGE_BYTES - BAR_BYTES;
   static constexpr int FIT = ROOM / SLOT_BYTES, MOST = 196608 / SLOT_BYTES;
   static constexpr int NSLOT = FIT < MOST ? FIT : MOST;
   static_assert(NSLOT > NC, "a tile's V slots are resident together while the next K slots pass");
   static constexpr int OFF_Q = NSLOT * SLOT_BYTES;
   static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;
   static constexpr int OFF_RED = OFF_P + 2 * P_BYTES;
-  static constexpr int OFF_BAR = OFF_RED + RED_BYTES;
+  static constexpr int OFF_PAGES = OFF_RED + RED_BYTES;
+  static constexpr int OFF_BAR = OFF_PAGES + PAGE_BYTES;
   // barriers
   static constexpr int B_FULL = 0, B_EMPTY = NSLOT, B_QFULL = 2 * NSLOT, B_QEMPTY = B_QFULL + 2, B_SFULL = B_QEMPTY + 2,
                        B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2, B_PDONE = B_PFULL + 2, B_DRAIN = B_PDONE + 2, NBAR = B_DRAIN + 1;
@@ -65,6 +69,16 @@ struct PagedCfg {
   static constexpr int T_COLS = T_USED <= 64 ? 64 : T_USED <= 128 ? 128 : T_USED <= 256 ? 256 : 512;
   static_assert(T_USED <= 512, "tensor memory");
 };
+
+// P^T is the B operand, MN-major: a row per key of 2 NH values (hi parts, then lo parts), 32, 64
+// or 128 bytes long, swizzled over that span (16-byte chunk index ^= (address >> 7) & 1, 3, 7),
+// so that a softmax thread stores its key's weights as whole vectors without bank conflicts.
+template <int NH>
+__device__ __forceinline__ uint64_t p_desc(uint32_t addr) {
+  const uint64_t d = sdesc_sw128(addr, 16, 8 * 4 * NH);  // 8 keys to the next group along K
+  constexpr uint64_t mode = NH == 8 ? 6 : NH == 16 ? 4 : 2;  // 32-, 64-, 128-byte swizzle
+  return (d & ~(7ull << 61)) | (mode << 61);
+}
 
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t (&r)[N]) {
@@ -78,6 +92,22 @@ __device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t (&r)[N]) {
   if constexpr (N == 16) tmem_st32x16(a, r);
   else if constexpr (N == 32) tmem_st32x32(a, r);
   else tmem_st32x64(a, r);
+}
+
+// Two weights as packed hi parts and packed lo parts, hi + lo = w up to the second rounding.
+template <bool BF>
+__device__ __forceinline__ void split_weights(float a, float b, uint32_t &hi, uint32_t &lo) {
+  hi = pack2<BF>(a, b);
+  float x, y;
+  if constexpr (BF) {
+    x = __uint_as_float(hi << 16);
+    y = __uint_as_float(hi & 0xffff0000u);
+  } else {
+    const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    x = t.x;
+    y = t.y;
+  }
+  lo = pack2<BF>(a - x, b - y);
 }
 
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -197,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < C::NSLOT; ++i) {
-      mbar_init(BAR(C::B_FULL + i), 1);
+      mbar_init(BAR(C::B_FULL + i), kProducers);
       mbar_init(BAR(C::B_EMPTY + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -273,42 +303,69 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Walk walk(p, misc.start_b, misc.start_off, T);
   bool ok = true;
 
-  if (warp == 4) {
-    // ---------------------------------------------------------- producer
+  if (warp >= 5) {
+    // ---------------------------------------------------------- producers
+    const int which = warp - 5;
     Tiles it(walk);
     const int rows = p.box_rows, chunks = kPagedTile / rows, lanes = chunks * C::NBOX;
     const int row = (lane / C::NBOX) * rows, box = lane % C::NBOX;  // this lane's box of a slot
-    long long at = 0;  // slots filled
+    const bool busy = lane < lanes && lane % kProducers == which;
+    uint32_t slot = 0, lap = 0, filled = 0;  // the ring slot next in turn, its phase, slots filled (up to NSLOT)
     int queries = 0;   // query tiles loaded
+    // Page numbers come through shared memory, asynchronously, kAhead tiles ahead: a producer that
+    // waited for each in a register would run at the table's latency.
+    const uint32_t mine_p = base + C::OFF_PAGES + (which * kAhead * 32 + lane) * 4;
+    Tiles pre(walk);
+    auto prefetch = [&](uint32_t stage) {
+      Tile t;
+      if (pre.next(t) && busy && row < t.n)
+        cp_async_4(mine_p + stage * 128, p.table + t.b * p.table_s + (t.pos + row) / p.page);
+      cp_async_commit();
+    };
+#pragma unroll
+    for (uint32_t i = 0; i < kAhead; ++i) prefetch(i);
     struct Load {
       Tile t;
       int page, slot;
     };
+    uint32_t stage = 0;
     auto look = [&](Load &l) -> bool {  // the next tile, and this lane's page of it
       if (!it.next(l.t)) return false;
       l.page = l.slot = 0;
-      if (row < l.t.n && lane < lanes) {
-        const int pos = l.t.pos + row, index = pos / p.page;
-        l.slot = pos - index * p.page;
-        l.page = p.table[l.t.b * p.table_s + index];
+      cp_async_wait<kAhead - 1>();
+      if (busy && row < l.t.n) {
+        l.slot = (l.t.pos + row) % p.page;
+        l.page = static_cast<int>(ld_shared_u32(mine_p + stage * 128));
       }
+      prefetch(stage);
+      stage = stage + 1 == kAhead ? 0 : stage + 1;
       return true;
     };
     auto fill = [&](const Load &l, const CUtensorMap *tm) {
       if (l.page < 0 || l.page >= p.pages) atomicCAS(p.status, 0u, kDevBadPage);  // TMA reads zeros there
-      const uint32_t bytes = static_cast<uint32_t>((l.t.n + rows - 1) / rows * rows) * 128u * C::NBOX;
+      const bool mine = busy && row < l.t.n;
+      const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, mine)) * rows) * 128u;
       const int head = l.t.hv / p.blocks;
-      for (int c = 0; ok && c < C::NC; ++c, ++at) {
-        const uint32_t slot = static_cast<uint32_t>(at % C::NSLOT);
-        if (at >= C::NSLOT)
-          ok = __all_sync(0xffffffffu, wait_bounded(BAR(C::B_EMPTY + slot), (at / C::NSLOT - 1) & 1, &misc.abort_flag, p.status,
-                                                    kDevTimeoutLoad, p.wait_limit));
-        if (!ok) break;
+      bool got = true;
+      for (int c = 0; c < C::NC; ++c) {
+        if (filled == C::NSLOT)
+          got = got && wait_bounded(BAR(C::B_EMPTY + slot), lap ^ 1u, &misc.abort_flag, p.status, kDevTimeoutLoad, p.wait_limit);
+        else
+          ++filled;
+        got = __all_sync(0xffffffffu, got);
+        if (!got) {
+          ok = false;
+          break;
+        }
         if (lane == 0) mbar_arrive_expect_tx(BAR(C::B_FULL + slot), bytes);
         __syncwarp();
-        if (lane < lanes && row < l.t.n)
+        if (mine)
           tma_load_4d(base + slot * C::SLOT_BYTES + box * C::BOX_BYTES + row * 128, tm, c * C::CW + box * 64, l.slot, head, l.page,
                       BAR(C::B_FULL + slot));
+        if (++slot == C::NSLOT) {
+          slot = 0;
+          lap ^= 1u;
+        }
       }
     };
     auto query = [&](const Tile &t) {  // Q of a segment, before its first K
@@ -316,17 +373,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (s >= 2)
         ok = __all_sync(0xffffffffu, wait_bounded(BAR(C::B_QEMPTY + (s & 1)), ((s - 2) >> 1) & 1, &misc.abort_flag, p.status,
                                                   kDevTimeoutLoad, p.wait_limit));
-      if (!ok || lane != 0) return;
+      if (!ok || lane != 0 || which != 0) return;
       queries = s + 1;
       const uint32_t bar = BAR(C::B_QFULL + (s & 1)), dst = base + C::OFF_Q + (s & 1) * C::Q_BYTES;
       mbar_arrive_expect_tx(bar, static_cast<uint32_t>(p.q_rows) * 128u * (D / 64));
       const int head = (t.hv / p.blocks) * p.G + (t.hv % p.blocks) * NH;
       for (int x = 0; x < D / 64; ++x) tma_load_3d(dst + x * C::NQ * 128, &tm_q, x * 64, head, t.b, bar);
     };
-    Load v, k, ahead;
+    Load v, k;
     bool have_v = false, have_k = look(k);
     while (ok && (have_k || have_v)) {
-      const bool have_a = have_k && look(ahead);
       if (have_k) {
         if (k.t.first) query(k.t);
         if (ok) fill(k, &tm_k);
@@ -334,84 +390,90 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && have_v) fill(v, &tm_v);
       v = k;
       have_v = have_k;
-      k = ahead;
-      have_k = have_a;
+      have_k = have_k && look(k);
     }
+    cp_async_wait<0>();
     // After a time-out: copies that nobody waited for land before the CTA ends.
-    if (lane == 0 && misc.abort_flag) {
-      for (long long x = max(0LL, at - C::NSLOT); x < at; ++x)
-        wait_drain(BAR(C::B_FULL + static_cast<int>(x % C::NSLOT)), (x / C::NSLOT) & 1, p.wait_limit);
+    if (lane == 0 && which == 0 && misc.abort_flag) {
+      for (uint32_t x = 0; x < filled; ++x)  // a slot before the next in turn was last filled in this lap
+        wait_drain(BAR(C::B_FULL + x), x < slot ? lap : lap ^ 1u, p.wait_limit);
       for (int x = max(0, queries - 2); x < queries; ++x) wait_drain(BAR(C::B_QFULL + (x & 1)), (x >> 1) & 1, p.wait_limit);
     }
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == 4) {
     // ---------------------------------------------------------- MMA issuer
     const uint32_t idesc_s = p.bf16 ? idesc_bf16_f32(128, C::NQ, 0, 0) : idesc_f16_f32(128, C::NQ, 0, 0);
-    const uint32_t idesc_o = p.bf16 ? idesc_bf16_f32(128, C::NP, 1, 0) : idesc_f16_f32(128, C::NP, 1, 0);
+    const uint32_t idesc_o = p.bf16 ? idesc_bf16_f32(128, C::NP, 1, 1) : idesc_f16_f32(128, C::NP, 1, 1);
     const SDesc dk = sdesc_split(sdesc_sw128(base, 16, 1024));
     // V^T: 64-column boxes BOX_BYTES apart; at d = 64 there is one, read twice (rows 64 .. of O are not used)
     const SDesc dv = sdesc_split(sdesc_sw128(base, C::NBOX == 1 ? 0 : C::BOX_BYTES, 1024));
     const SDesc dq = sdesc_split(sdesc_sw128(base + C::OFF_Q, 16, 1024));
-    const SDesc dp = sdesc_split(sdesc_sw128(base + C::OFF_P, 16, 1024));
-    auto wait = [&](int bar, long long phase) {
-      ok = ok && __all_sync(0xffffffffu, wait_bounded(BAR(bar), static_cast<uint32_t>(phase & 1), &misc.abort_flag, p.status, kDevTimeoutMma,
-                                                      p.wait_limit));
+    const SDesc dp = sdesc_split(p_desc<NH>(base + C::OFF_P));
+    // Every lane waits, lane 0 issues; whether all waits passed is agreed on once per product.
+    bool got = true;
+    auto wait = [&](int bar, uint32_t phase) {
+      got = got && wait_bounded(BAR(bar), phase & 1u, &misc.abort_flag, p.status, kDevTimeoutMma, p.wait_limit);
     };
-    long long at = 0;
-    Tiles it(walk);
-    Tile cur, nxt;
-    auto qk = [&](const Tile &t, long long i) {
-      const int buf = static_cast<int>(i & 1), qb = t.seg & 1;
-      if (t.first) wait(C::B_QFULL + qb, t.seg >> 1);
+    uint32_t slot = 0, lap = 0;  // the ring slot next in turn, and its phase
+    auto step = [&]() {
+      if (++slot == C::NSLOT) {
+        slot = 0;
+        lap ^= 1u;
+      }
+    };
+    auto qk = [&](uint32_t i, uint32_t seg, bool first, bool last) {
+      const uint32_t buf = i & 1u, qb = seg & 1u;
+      if (first) wait(C::B_QFULL + qb, seg >> 1);
       if (i >= 2) wait(C::B_SFREE + buf, (i - 2) >> 1);
-      for (int c = 0; ok && c < C::NC; ++c, ++at) {
-        const uint32_t slot = static_cast<uint32_t>(at % C::NSLOT);
-        wait(C::B_FULL + slot, at / C::NSLOT);
-        if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
+      for (int c = 0; c < C::NC; ++c, step()) {
+        wait(C::B_FULL + slot, lap);
+        if (lane == 0 && got) {
+          tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < C::CW / 16; ++kk)
             umma_ss_off(tmem + buf * C::NQ, dk, slot * C::SLOT_BYTES + (kk >> 2) * C::BOX_BYTES + (kk & 3) * 32, dq,
                         qb * C::Q_BYTES + (c * C::NBOX + (kk >> 2)) * C::NQ * 128 + (kk & 3) * 32, idesc_s, (c | kk) != 0);
           umma_commit(BAR(C::B_EMPTY + slot));
         }
-        __syncwarp();
       }
-      if (ok && lane == 0) {
+      if (lane == 0 && got) {
         umma_commit(BAR(C::B_SFULL + buf));
-        if (t.last) umma_commit(BAR(C::B_QEMPTY + qb));
+        if (last) umma_commit(BAR(C::B_QEMPTY + qb));
       }
-      __syncwarp();
+      got = __all_sync(0xffffffffu, got);
     };
-    auto pv = [&](const Tile &t, long long i) {
-      const int buf = static_cast<int>(i & 1);
+    auto pv = [&](uint32_t i, bool first) {
+      const uint32_t buf = i & 1u;
       wait(C::B_PFULL + buf, i >> 1);
-      for (int c = 0; ok && c < C::NC; ++c, ++at) {
-        const uint32_t slot = static_cast<uint32_t>(at % C::NSLOT);
-        wait(C::B_FULL + slot, at / C::NSLOT);
-        if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
+      for (int c = 0; c < C::NC; ++c, step()) {
+        wait(C::B_FULL + slot, lap);
+        if (lane == 0 && got) {
+          tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < kPagedTile / 16; ++kk)
-            umma_ss_off(tmem + C::T_O + c * C::NP, dv, slot * C::SLOT_BYTES + kk * 2048, dp,
-                        buf * C::P_BYTES + (kk >> 2) * C::NP * 128 + (kk & 3) * 32, idesc_o, !t.first || kk > 0);
+            umma_ss_off(tmem + C::T_O + c * C::NP, dv, slot * C::SLOT_BYTES + kk * 2048, dp, buf * C::P_BYTES + kk * (16 * 4 * NH), idesc_o,
+                        !first || kk > 0);
           umma_commit(BAR(C::B_EMPTY + slot));
         }
-        __syncwarp();
       }
-      if (ok && lane == 0) umma_commit(BAR(C::B_PDONE + buf));
-      __syncwarp();
+      if (lane == 0 && got) umma_commit(BAR(C::B_PDONE + buf));
+      got = __all_sync(0xffffffffu, got);
     };
-    bool have = it.next(cur);
-    if (have) qk(cur, 0);
-    for (long long i = 0; ok && have; ++i) {
-      have = it.next(nxt);
-      if (have) qk(nxt, i + 1);
-      if (ok) pv(cur, i);
-      cur = nxt;
+    // QK a tile ahead of PV; a segment is looked up when its first QK is due.
+    Walk w(walk);
+    Seg s;
+    uint32_t i = 0, seg = 0;
+    bool pending = false, pending_first = false;  // PV(i - 1) is due
+    while (got && w.next(s)) {
+      for (int j = 0; got && j < s.count; ++j, ++i) {
+        qk(i, seg, j == 0, j == s.count - 1);
+        if (got && pending) pv(i - 1, pending_first);
+        pending = true;
+        pending_first = j == 0;
+      }
+      ++seg;
     }
+    if (got && pending) pv(i - 1, pending_first);
     if (misc.abort_flag && lane == 0) {  // after a time-out: products in flight end before the CTA does
       umma_commit(BAR(C::B_DRAIN));
       wait_drain(BAR(C::B_DRAIN), 0, p.wait_limit);
@@ -454,13 +516,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(BAR(C::B_SFREE + buf));
         float top[NH];
 #pragma unroll
-        for (int h = 0; h < NH; ++h)
-          if (h < heads) {
-            const float v = tid < n ? __uint_as_float(x[h]) * p.c2 : -INFINITY;
-            x[h] = __float_as_uint(v);
-            top[h] = warp_max(v);
+        for (int g = 0; g < NH; g += 8)
+          if (g < heads) {  // eight at a time, without branches between them
+#pragma unroll
+            for (int h = g; h < g + 8; ++h) {
+              const float v = tid < n ? __uint_as_float(x[h]) * p.c2 : -INFINITY;
+              x[h] = __float_as_uint(v);
+              top[h] = warp_max(v);
+            }
           } else {
-            top[h] = 0.f;
+#pragma unroll
+            for (int h = g; h < g + 8; ++h) top[h] = 0.f;
           }
         float *const mine_r = red + (buf * 4 + warp) * NH;
         if (lane == 0) {
@@ -469,48 +535,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         softmax_sync();
         // ---- the running maximum, and what it does to the sums and to O
-        bool moved = false;
         float keep[NH];
+        int moved = 0;  // the same in every thread
 #pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          keep[h] = 1.f;
-          if (h < heads) {
-            const float *const r = red + buf * 4 * NH + h;
-            const float t = fmaxf(fmaxf(r[0], r[NH]), fmaxf(r[2 * NH], r[3 * NH]));
-            if (j == 0 || t > m[h] + kSlack) {
-              if (j > 0) {
-                keep[h] = ex2_approx(m[h] - t);
-                l[h] *= keep[h];
-                moved = true;
-              }
-              m[h] = t;
-            }
+        for (int g = 0; g < NH; g += 4)
+          if (g < heads) {
+            const float4 *const r = reinterpret_cast<const float4 *>(red + buf * 4 * NH + g);
+            const float4 r0 = r[0], r1 = r[NH / 4], r2 = r[2 * NH / 4], r3 = r[3 * NH / 4];
+            top[g] = fmaxf(fmaxf(r0.x, r1.x), fmaxf(r2.x, r3.x));
+            top[g + 1] = fmaxf(fmaxf(r0.y, r1.y), fmaxf(r2.y, r3.y));
+            top[g + 2] = fmaxf(fmaxf(r0.z, r1.z), fmaxf(r2.z, r3.z));
+            top[g + 3] = fmaxf(fmaxf(r0.w, r1.w), fmaxf(r2.w, r3.w));
+#pragma unroll
+            for (int h = g; h < g + 4; ++h) moved |= static_cast<int>(h < heads) & static_cast<int>(top[h] > m[h] + kSlack);
+          }
+        if (j == 0) {
+          moved = 0;
+#pragma unroll
+          for (int h = 0; h < NH; ++h) m[h] = top[h];
+        } else if (moved) {
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            const bool up = top[h] > m[h] + kSlack;
+            keep[h] = up ? ex2_approx(m[h] - top[h]) : 1.f;
+            l[h] *= keep[h];
+            m[h] = up ? top[h] : m[h];
           }
         }
         // ---- the weights of this thread's key, as hi + lo
         if (i >= 2) wait(C::B_PDONE + buf, (i - 2) >> 1);
-        const uint32_t prow = base + C::OFF_P + buf * C::P_BYTES + (tid >> 6) * (C::NP * 128) + (tid & 7) * 2;
-        const uint32_t pcol = (tid & 63) >> 3;
+        const uint32_t prow = base + C::OFF_P + buf * C::P_BYTES + tid * (4 * NH);
+        const uint32_t swz = NH == 8 ? (tid >> 2) & 1 : NH == 16 ? (tid >> 1) & 3 : tid & 7;
 #pragma unroll
-        for (int h = 0; h < NH; ++h)
-          if (h < heads) {
-            const float e = ex2_approx(__uint_as_float(x[h]) - (m[h] == -INFINITY ? 0.f : m[h] - kShift));
-            l[h] += e;
-            uint32_t parts;
-            if (p.bf16) {
-              const __nv_bfloat16 hi = __float2bfloat16_rn(e);
-              const __nv_bfloat16 lo = __float2bfloat16_rn(e - __bfloat162float(hi));
-              parts = __bfloat16_as_ushort(hi) | (static_cast<uint32_t>(__bfloat16_as_ushort(lo)) << 16);
-            } else {
-              const __half hi = __float2half_rn(e);
-              const __half lo = __float2half_rn(e - __half2float(hi));
-              parts = __half_as_ushort(hi) | (static_cast<uint32_t>(__half_as_ushort(lo)) << 16);
+        for (int g = 0; g < NH; g += 8)
+          if (g < heads) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int h = g; h < g + 8; ++h) {
+              const float w = ex2_approx(__uint_as_float(x[h]) - (m[h] == -INFINITY ? 0.f : m[h] - kShift));
+              l[h] += w;
+              x[h] = __float_as_uint(w);
             }
-            const uint32_t a = prow + h * 128 + ((pcol ^ (h & 7)) << 4);  // row NH + h has the same swizzle (NH % 8 = 0)
-            asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"(static_cast<uint16_t>(parts)) : "memory");
-            asm volatile("st.shared.b16 [%0], %1;" ::"r"(a + NH * 128), "h"(static_cast<uint16_t>(parts >> 16)) : "memory");
+            if (p.bf16) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                split_weights<true>(__uint_as_float(x[g + 2 * e]), __uint_as_float(x[g + 2 * e + 1]), hi[e], lo[e]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                split_weights<false>(__uint_as_float(x[g + 2 * e]), __uint_as_float(x[g + 2 * e + 1]), hi[e], lo[e]);
+            }
+            st_shared_v4(prow + (((g >> 3) ^ swz) << 4), hi[0], hi[1], hi[2], hi[3]);
+            st_shared_v4(prow + ((((NH + g) >> 3) ^ swz) << 4), lo[0], lo[1], lo[2], lo[3]);
           }
-        if (moved) {  // the same in every thread
+        if (moved) {
           wait(C::B_PDONE + (buf ^ 1), (i - 1) >> 1);
           if (ok) {
             tc_fence_after();
