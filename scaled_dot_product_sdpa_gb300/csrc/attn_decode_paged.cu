@@ -52,6 +52,11 @@ struct PagedCfg {
   static constexpr int ROOM = 232448 - 1024 - 2 * Q_BYTES - 2 * P_BYTES - RED_BYTES - PAGE_BYTES - BAR_BYTES;
   static constexpr int FIT = ROOM / SLOT_BYTES, MOST = 196608 / SLOT_BYTES;
   static constexpr int NSLOT = FIT < MOST ? FIT : MOST;
+  // With one slot a tile, the commit that frees K's slot also tells that S is there, and the one that
+  // frees V's that PV is done (a commit costs its thread about 190 cycles); nothing else is
+  // committed to that slot before the softmax has looked, as the ring holds more than four tiles' slots.
+  static constexpr bool ONE = NC == 1;
+  static_assert(!ONE || NSLOT >= 5, "slots that the softmax waits on");
   static_assert(NSLOT > NC, "a tile's V slots are resident together while the next K slots pass");
   static constexpr int OFF_Q = NSLOT * SLOT_BYTES;
   static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;
@@ -60,7 +65,7 @@ struct PagedCfg {
   static constexpr int OFF_BAR = OFF_PAGES + PAGE_BYTES;
   // barriers
   static constexpr int B_FULL = 0, B_EMPTY = NSLOT, B_QFULL = 2 * NSLOT, B_QEMPTY = B_QFULL + 2, B_SFULL = B_QEMPTY + 2,
-                       B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2, B_PDONE = B_PFULL + 2, B_DRAIN = B_PDONE + 2, NBAR = B_DRAIN + 1;
+                       B_PFULL = B_SFULL + 2, B_PDONE = B_PFULL + 2, B_DRAIN = B_PDONE + 2, NBAR = B_DRAIN + 1;
   static constexpr int SMEM_BYTES = 1024 + OFF_BAR + BAR_BYTES;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
   static constexpr int NO = D <= 128 ? 1 : D / 128;     // 128-column blocks of O
@@ -124,31 +129,52 @@ struct Seg {
   int b, hv, len, tile, count, tiles;  // tiles: of the whole row
 };
 
-// Walks over a CTA's share, all lanes of a warp alike; 32 lengths are held at a time.
+// A row's place: sequence and offset of a CTA's first unit in it, and the share's units.
+struct Start {
+  int b;
+  long long off, units;
+};
+
+// Walks over a CTA's share.  By a warp, whose lanes hold 32 lengths at a time, or by one thread,
+// which has the next sequence's length on the way.
+template <bool WARP>
 struct Walk {
-  int b, hv, tile, hvs, base, held;
+  int b, hv = 0, tile = 0, hvs, len = 0, ahead = 0, base;
   long long left;
   const PagedParams &p;
-  __device__ Walk(const PagedParams &pp, int b0, long long off, long long n) : p(pp) {
+  __device__ Walk(const PagedParams &pp, const Start &at) : p(pp) {
     hvs = pp.Hkv * pp.blocks;
-    b = b0;
-    left = n;
-    base = b0;
-    hv = tile = 0;
-    held = 0;
-    if (left > 0) {
-      fetch();
-      const int nt = tiles_of(length());
-      hv = static_cast<int>(off / nt);
-      tile = static_cast<int>(off - static_cast<long long>(hv) * nt);
-    }
+    b = base = at.b;
+    left = at.units;
+    if (left <= 0) return;
+    fetch();
+    const int nt = tiles_of(length());
+    hv = static_cast<int>(at.off / nt);
+    tile = static_cast<int>(at.off - static_cast<long long>(hv) * nt);
   }
+  __device__ int load(int i) const { return i < p.B ? clamp_length(p.lengths[i], p) : 0; }
   __device__ void fetch() {
     base = b;
-    const int i = b + static_cast<int>(threadIdx.x & 31);
-    held = i < p.B ? clamp_length(p.lengths[i], p) : 0;
+    if constexpr (WARP) {
+      len = load(b + static_cast<int>(threadIdx.x & 31));
+    } else {
+      len = load(b);
+      ahead = load(b + 1);
+    }
   }
-  __device__ int length() const { return __shfl_sync(0xffffffffu, held, b - base); }
+  __device__ int length() const {
+    if constexpr (WARP) return __shfl_sync(0xffffffffu, len, b - base);
+    return len;
+  }
+  __device__ void advance() {  // to sequence b + 1
+    ++b;
+    if constexpr (WARP) {
+      if (b - base == 32 && b < p.B) fetch();
+    } else {
+      len = ahead;
+      ahead = load(b + 1);
+    }
+  }
   __device__ bool next(Seg &s) {
     if (left <= 0) return false;
     s.b = b;
@@ -163,9 +189,8 @@ struct Walk {
       tile = 0;
       if (++hv == hvs) {
         hv = 0;
-        do {
-          if (++b - base == 32 && b < p.B) fetch();
-        } while (left > 0 && b < p.B && length() == 0);
+        do advance();
+        while (left > 0 && b < p.B && length() == 0);
       }
     }
     return true;
@@ -179,10 +204,10 @@ struct Tile {
   bool first, last;   // of its segment
 };
 struct Tiles {
-  Walk w;
+  Walk<true> w;
   Seg s;
   int i = 0, seg = -1;
-  __device__ Tiles(const Walk &walk) : w(walk) { s.count = 0; }
+  __device__ Tiles(const PagedParams &p, const Start &at) : w(p, at) { s.count = 0; }
   __device__ bool next(Tile &t) {
     if (i == s.count) {
       if (!w.next(s)) return false;
@@ -200,8 +225,9 @@ struct Tiles {
   }
 };
 
-// Where a tile's V begins in the ring's order K0 K1 V0 K2 V1 ... (T tiles, nc slots each).
-__device__ __forceinline__ long long v_pos(long long t, long long T, int nc) { return (min(t + 2, T) + t) * nc; }
+// Where a tile's K and V begin in the ring's order K0 K1 V0 K2 V1 ... (T tiles, nc slots each).
+__device__ __forceinline__ uint32_t k_pos(uint32_t t, int nc) { return t == 0 ? 0 : (2 * t - 1) * nc; }
+__device__ __forceinline__ uint32_t v_pos(uint32_t t, uint32_t T, int nc) { return (min(t + 2, T) + t) * nc; }
 
 template <int D, int NH>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -234,7 +260,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(BAR(C::B_QFULL + i), 1);
       mbar_init(BAR(C::B_QEMPTY + i), 1);
       mbar_init(BAR(C::B_SFULL + i), 1);
-      mbar_init(BAR(C::B_SFREE + i), 4);
       mbar_init(BAR(C::B_PFULL + i), 4);
       mbar_init(BAR(C::B_PDONE + i), 1);
     }
@@ -300,13 +325,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = misc.tmem_base;
   const long long T = u1 - u0;
-  const Walk walk(p, misc.start_b, misc.start_off, T);
+  const Start start = {misc.start_b, misc.start_off, T};
   bool ok = true;
 
   if (warp >= 5) {
     // ---------------------------------------------------------- producers
     const int which = warp - 5;
-    Tiles it(walk);
+    Tiles it(p, start);
     const int rows = p.box_rows, chunks = kPagedTile / rows, lanes = chunks * C::NBOX;
     const int row = (lane / C::NBOX) * rows, box = lane % C::NBOX;  // this lane's box of a slot
     const bool busy = lane < lanes && lane % kProducers == which;
@@ -315,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Page numbers come through shared memory, asynchronously, kAhead tiles ahead: a producer that
     // waited for each in a register would run at the table's latency.
     const uint32_t mine_p = base + C::OFF_PAGES + (which * kAhead * 32 + lane) * 4;
-    Tiles pre(walk);
+    Tiles pre(p, start);
     auto prefetch = [&](uint32_t stage) {
       Tile t;
       if (pre.next(t) && busy && row < t.n)
@@ -393,11 +418,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       have_k = have_k && look(k);
     }
     cp_async_wait<0>();
-    // After a time-out: copies that nobody waited for land before the CTA ends.
-    if (lane == 0 && which == 0 && misc.abort_flag) {
-      for (uint32_t x = 0; x < filled; ++x)  // a slot before the next in turn was last filled in this lap
-        wait_drain(BAR(C::B_FULL + x), x < slot ? lap : lap ^ 1u, p.wait_limit);
-      for (int x = max(0, queries - 2); x < queries; ++x) wait_drain(BAR(C::B_QFULL + (x & 1)), (x >> 1) & 1, p.wait_limit);
+    // After a time-out: copies that nobody waited for land before the CTA ends (a slot before the
+    // next in turn was last filled in this lap; one that not every producer filled never completes,
+    // and gets some milliseconds).
+    if (lane == 0 && misc.abort_flag) {
+      for (uint32_t x = 0; x < filled; ++x) wait_drain(BAR(C::B_FULL + x), x < slot ? lap : lap ^ 1u, p.wait_limit >> 10);
+      for (int x = max(0, queries - 2); x < queries; ++x) wait_drain(BAR(C::B_QFULL + (x & 1)), (x >> 1) & 1, p.wait_limit >> 10);
     }
     __syncwarp();
   } else if (warp == 4) {
@@ -409,74 +435,75 @@ __global__ void __launch_bounds__(kThreads, 1)
     const SDesc dv = sdesc_split(sdesc_sw128(base, C::NBOX == 1 ? 0 : C::BOX_BYTES, 1024));
     const SDesc dq = sdesc_split(sdesc_sw128(base + C::OFF_Q, 16, 1024));
     const SDesc dp = sdesc_split(p_desc<NH>(base + C::OFF_P));
-    // Every lane waits, lane 0 issues; whether all waits passed is agreed on once per product.
-    bool got = true;
-    auto wait = [&](int bar, uint32_t phase) {
-      got = got && wait_bounded(BAR(bar), phase & 1u, &misc.abort_flag, p.status, kDevTimeoutMma, p.wait_limit);
-    };
-    uint32_t slot = 0, lap = 0;  // the ring slot next in turn, and its phase
-    auto step = [&]() {
-      if (++slot == C::NSLOT) {
-        slot = 0;
-        lap ^= 1u;
-      }
-    };
-    auto qk = [&](uint32_t i, uint32_t seg, bool first, bool last) {
-      const uint32_t buf = i & 1u, qb = seg & 1u;
-      if (first) wait(C::B_QFULL + qb, seg >> 1);
-      if (i >= 2) wait(C::B_SFREE + buf, (i - 2) >> 1);
-      for (int c = 0; c < C::NC; ++c, step()) {
-        wait(C::B_FULL + slot, lap);
-        if (lane == 0 && got) {
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < C::CW / 16; ++kk)
-            umma_ss_off(tmem + buf * C::NQ, dk, slot * C::SLOT_BYTES + (kk >> 2) * C::BOX_BYTES + (kk & 3) * 32, dq,
-                        qb * C::Q_BYTES + (c * C::NBOX + (kk >> 2)) * C::NQ * 128 + (kk & 3) * 32, idesc_s, (c | kk) != 0);
-          umma_commit(BAR(C::B_EMPTY + slot));
+    if (lane == 0) {
+      // One thread waits and issues: no lane has to agree on anything, and a product's set-up is not
+      // paid for in votes (about 500 of 2100 cycles a tile, d = 64).
+      bool got = true;
+      auto wait = [&](int bar, uint32_t phase) {
+        got = got && wait_bounded(BAR(bar), phase & 1u, &misc.abort_flag, p.status, kDevTimeoutMma, p.wait_limit);
+      };
+      uint32_t slot = 0, lap = 0;  // the ring slot next in turn, and its phase
+      auto step = [&]() {
+        if (++slot == C::NSLOT) {
+          slot = 0;
+          lap ^= 1u;
         }
-      }
-      if (lane == 0 && got) {
-        umma_commit(BAR(C::B_SFULL + buf));
-        if (last) umma_commit(BAR(C::B_QEMPTY + qb));
-      }
-      got = __all_sync(0xffffffffu, got);
-    };
-    auto pv = [&](uint32_t i, bool first) {
-      const uint32_t buf = i & 1u;
-      wait(C::B_PFULL + buf, i >> 1);
-      for (int c = 0; c < C::NC; ++c, step()) {
-        wait(C::B_FULL + slot, lap);
-        if (lane == 0 && got) {
-          tc_fence_after();
+      };
+      auto qk = [&](uint32_t i, uint32_t seg, bool first, bool last) {
+        const uint32_t buf = i & 1u, qb = seg & 1u;
+        if (first) wait(C::B_QFULL + qb, seg >> 1);
+        // S(i - 2) has been read: PV(i - 2), issued before, waited for the weights made of it.
+        for (int c = 0; c < C::NC; ++c, step()) {
+          wait(C::B_FULL + slot, lap);
+          if (got) {
+            tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < kPagedTile / 16; ++kk)
-            umma_ss_off(tmem + C::T_O + c * C::NP, dv, slot * C::SLOT_BYTES + kk * 2048, dp, buf * C::P_BYTES + kk * (16 * 4 * NH), idesc_o,
-                        !first || kk > 0);
-          umma_commit(BAR(C::B_EMPTY + slot));
+            for (int kk = 0; kk < C::CW / 16; ++kk)
+              umma_ss_off(tmem + buf * C::NQ, dk, slot * C::SLOT_BYTES + (kk >> 2) * C::BOX_BYTES + (kk & 3) * 32, dq,
+                          qb * C::Q_BYTES + (c * C::NBOX + (kk >> 2)) * C::NQ * 128 + (kk & 3) * 32, idesc_s, (c | kk) != 0);
+            umma_commit(BAR(C::B_EMPTY + slot));
+          }
         }
+        if (got) {
+          if (!C::ONE) umma_commit(BAR(C::B_SFULL + buf));
+          if (last) umma_commit(BAR(C::B_QEMPTY + qb));
+        }
+      };
+      auto pv = [&](uint32_t i, bool first) {
+        const uint32_t buf = i & 1u;
+        wait(C::B_PFULL + buf, i >> 1);
+        for (int c = 0; c < C::NC; ++c, step()) {
+          wait(C::B_FULL + slot, lap);
+          if (got) {
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < kPagedTile / 16; ++kk)
+              umma_ss_off(tmem + C::T_O + c * C::NP, dv, slot * C::SLOT_BYTES + kk * 2048, dp, buf * C::P_BYTES + kk * (16 * 4 * NH), idesc_o,
+                          !first || kk > 0);
+            umma_commit(BAR(C::B_EMPTY + slot));
+          }
+        }
+        if (!C::ONE && got) umma_commit(BAR(C::B_PDONE + buf));
+      };
+      // QK a tile ahead of PV; a segment is looked up when its first QK is due.
+      Walk<false> w(p, start);
+      Seg s;
+      uint32_t i = 0, seg = 0;
+      bool pending = false, pending_first = false;  // PV(i - 1) is due
+      while (got && w.next(s)) {
+        for (int j = 0; got && j < s.count; ++j, ++i) {
+          qk(i, seg, j == 0, j == s.count - 1);
+          if (got && pending) pv(i - 1, pending_first);
+          pending = true;
+          pending_first = j == 0;
+        }
+        ++seg;
       }
-      if (lane == 0 && got) umma_commit(BAR(C::B_PDONE + buf));
-      got = __all_sync(0xffffffffu, got);
-    };
-    // QK a tile ahead of PV; a segment is looked up when its first QK is due.
-    Walk w(walk);
-    Seg s;
-    uint32_t i = 0, seg = 0;
-    bool pending = false, pending_first = false;  // PV(i - 1) is due
-    while (got && w.next(s)) {
-      for (int j = 0; got && j < s.count; ++j, ++i) {
-        qk(i, seg, j == 0, j == s.count - 1);
-        if (got && pending) pv(i - 1, pending_first);
-        pending = true;
-        pending_first = j == 0;
+      if (got && pending) pv(i - 1, pending_first);
+      if (misc.abort_flag) {  // after a time-out: products in flight end before the CTA does
+        umma_commit(BAR(C::B_DRAIN));
+        wait_drain(BAR(C::B_DRAIN), 0, p.wait_limit);
       }
-      ++seg;
-    }
-    if (got && pending) pv(i - 1, pending_first);
-    if (misc.abort_flag && lane == 0) {  // after a time-out: products in flight end before the CTA does
-      umma_commit(BAR(C::B_DRAIN));
-      wait_drain(BAR(C::B_DRAIN), 0, p.wait_limit);
     }
     __syncwarp();
   } else {
@@ -489,13 +516,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = tid; i < p.Hq; i += 128) p.lse[static_cast<size_t>(b) * p.Hq + i] = -INFINITY;
       }
     PagedRecord record = {0, 0, 0, 0};
-    auto wait = [&](int bar, long long phase) {
+    auto wait = [&](int bar, uint32_t phase) {
       ok = __all_sync(0xffffffffu, wait_bounded(BAR(bar), static_cast<uint32_t>(phase & 1), &misc.abort_flag, p.status, kDevTimeoutSoftmax,
                                                 p.wait_limit)) && ok;
     };
-    Walk w(walk);
+    auto wait_s = [&](uint32_t t) {  // S of tile t is there
+      const uint32_t x = k_pos(t, 1);
+      if (C::ONE)
+        wait(C::B_EMPTY + static_cast<int>(x % C::NSLOT), x / C::NSLOT);
+      else
+        wait(C::B_SFULL + static_cast<int>(t & 1), t >> 1);
+    };
+    const uint32_t tiles = static_cast<uint32_t>(T);
+    auto wait_pv = [&](uint32_t t) {  // PV of tile t is done
+      const uint32_t x = v_pos(t, tiles, 1);
+      if (C::ONE)
+        wait(C::B_EMPTY + static_cast<int>(x % C::NSLOT), x / C::NSLOT);
+      else
+        wait(C::B_PDONE + static_cast<int>(t & 1), t >> 1);
+    };
+    Walk<true> w(p, start);
     Seg s;
-    long long i = 0;  // tiles done
+    uint32_t i = 0;  // tiles done
     while (w.next(s)) {
       const int block = s.hv % p.blocks, heads = min(NH, p.G - block * NH);
       float m[NH], l[NH];
@@ -508,12 +550,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // After a time-out the remaining tiles run through the barriers only.
         const int buf = static_cast<int>(i & 1), n = s.len - (s.tile + j) * kPagedTile;
         uint32_t x[NH];
-        wait(C::B_SFULL + buf, i >> 1);
+        wait_s(i);
         tc_fence_after();
         tmem_ld<NH>(lanes + buf * C::NQ, x);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(C::B_SFREE + buf));
         float top[NH];
 #pragma unroll
         for (int g = 0; g < NH; g += 8)
@@ -563,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // ---- the weights of this thread's key, as hi + lo
-        if (i >= 2) wait(C::B_PDONE + buf, (i - 2) >> 1);
+        if (i >= 2) wait_pv(i - 2);
         const uint32_t prow = base + C::OFF_P + buf * C::P_BYTES + tid * (4 * NH);
         const uint32_t swz = NH == 8 ? (tid >> 2) & 1 : NH == 16 ? (tid >> 1) & 3 : tid & 7;
 #pragma unroll
@@ -589,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             st_shared_v4(prow + ((((NH + g) >> 3) ^ swz) << 4), lo[0], lo[1], lo[2], lo[3]);
           }
         if (moved) {
-          wait(C::B_PDONE + (buf ^ 1), (i - 1) >> 1);
+          wait_pv(i - 1);
           if (ok) {
             tc_fence_after();
 #pragma unroll
@@ -608,10 +647,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n < kPagedTile) {
           // Whatever lies behind the last token (unwritten slots, earlier tiles) times a weight of
           // zero must be zero: clear those rows of V.
-          const long long v0 = v_pos(i, T, C::NC);
+          if (!C::ONE) {
+            // The slots' earlier loads, of V(i - 1) and K(i + 1), must be past, or a wait for V's load
+            // would take the phase before theirs for it.
+            if (i >= 1) wait_pv(i - 1);
+            if (i + 1 < tiles) wait_s(i + 1);
+          }
+          const uint32_t v0 = v_pos(i, tiles, C::NC);
           for (int c = 0; c < C::NC; ++c) {
-            const uint32_t slot = static_cast<uint32_t>((v0 + c) % C::NSLOT);
-            wait(C::B_FULL + slot, (v0 + c) / C::NSLOT);
+            const uint32_t slot = (v0 + c) % C::NSLOT;
+            wait(C::B_FULL + static_cast<int>(slot), (v0 + c) / C::NSLOT);
             if (ok && tid >= n)
 #pragma unroll
               for (int z = 0; z < C::NBOX * 8; ++z)
@@ -634,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) sums[warp * NH + h] = t;
         }
       softmax_sync();
-      wait(C::B_PDONE + static_cast<int>((i - 1) & 1), (i - 1) >> 1);
+      wait_pv(i - 1);
       tc_fence_after();
       const bool whole = s.count == s.tiles, begins = s.tile == 0;
       const int head0 = (s.hv / p.blocks) * p.G + block * NH;
