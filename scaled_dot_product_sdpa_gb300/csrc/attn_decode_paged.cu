@@ -197,32 +197,36 @@ struct Walk {
   }
 };
 
-// The same, tile by tile.
-struct Tile {
-  int b, hv, n, pos;  // valid keys in the tile; its first position
-  int seg;            // number of its segment within the share
-  bool first, last;   // of its segment
-};
-struct Tiles {
-  Walk<true> w;
+// The same by one thread, tile by tile, with the page and slot of the tile's row `row` (a page's
+// slots follow one another through the tiles of a segment, so that only its first tile divides).
+struct Cursor {
+  Walk<false> w;
   Seg s;
-  int i = 0, seg = -1;
-  __device__ Tiles(const PagedParams &p, const Start &at) : w(p, at) { s.count = 0; }
-  __device__ bool next(Tile &t) {
+  int i = 0, seg = -1, row, index = 0, slot = 0;  // index: in the sequence's table row
+  __device__ Cursor(const PagedParams &p, const Start &at, int r) : w(p, at), row(r) { s.count = 0; }
+  __device__ bool next() {
+    const int page = w.p.page;
     if (i == s.count) {
       if (!w.next(s)) return false;
       i = 0;
       ++seg;
+      const int pos = s.tile * kPagedTile + row;
+      index = pos / page;
+      slot = pos - index * page;
+    } else {
+      index += w.p.tile_pages;
+      slot += w.p.tile_slots;
+      if (slot >= page) {
+        slot -= page;
+        ++index;
+      }
     }
-    t.b = s.b;
-    t.hv = s.hv;
-    t.pos = (s.tile + i) * kPagedTile;
-    t.n = min(kPagedTile, s.len - t.pos);
-    t.seg = seg;
-    t.first = i == 0;
-    t.last = ++i == s.count;
+    ++i;
     return true;
   }
+  // valid keys in the tile
+  __device__ int keys() const { return min(kPagedTile, s.len - (s.tile + i - 1) * kPagedTile); }
+  __device__ bool first() const { return i == 1; }
 };
 
 // Where a tile's K and V begin in the ring's order K0 K1 V0 K2 V1 ... (T tiles, nc slots each).
@@ -331,61 +335,57 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 5) {
     // ---------------------------------------------------------- producers
     const int which = warp - 5;
-    Tiles it(p, start);
-    const int rows = p.box_rows, chunks = kPagedTile / rows, lanes = chunks * C::NBOX;
+    // Every lane runs on its own: it waits for a slot and copies its box, if it has one in the tile
+    // (boxes of K and V are dealt out over the producers); lane 0 also announces the producer's bytes.
+    const int rows = p.box_rows, lanes = kPagedTile / rows * C::NBOX;
     const int row = (lane / C::NBOX) * rows, box = lane % C::NBOX;  // this lane's box of a slot
-    const bool busy = lane < lanes && lane % kProducers == which;
+    const bool deals_k = lane < lanes && lane % kProducers == which;
+    const bool deals_v = lane < lanes && (lanes + lane) % kProducers == which;
+    const bool deals = deals_k || deals_v;
     uint32_t slot = 0, lap = 0, filled = 0;  // the ring slot next in turn, its phase, slots filled (up to NSLOT)
-    int queries = 0;   // query tiles loaded
+    int queries = 0;                         // query tiles loaded
     // Page numbers come through shared memory, asynchronously, kAhead tiles ahead: a producer that
     // waited for each in a register would run at the table's latency.
     const uint32_t mine_p = base + C::OFF_PAGES + (which * kAhead * 32 + lane) * 4;
-    Tiles pre(p, start);
-    auto prefetch = [&](uint32_t stage) {
-      Tile t;
-      if (pre.next(t) && busy && row < t.n)
-        cp_async_4(mine_p + stage * 128, p.table + t.b * p.table_s + (t.pos + row) / p.page);
+    Cursor pre(p, start, row), it(p, start, row);
+    uint32_t stage = 0;
+    auto prefetch = [&]() {
+      if (deals && pre.next() && row < pre.keys()) cp_async_4(mine_p + stage * 128, p.table + pre.s.b * p.table_s + pre.index);
       cp_async_commit();
+      stage = stage + 1 == kAhead ? 0 : stage + 1;
     };
 #pragma unroll
-    for (uint32_t i = 0; i < kAhead; ++i) prefetch(i);
+    for (int i = 0; i < kAhead; ++i) prefetch();
     struct Load {
-      Tile t;
-      int page, slot;
+      int keys, head, page, slot;
     };
-    uint32_t stage = 0;
     auto look = [&](Load &l) -> bool {  // the next tile, and this lane's page of it
-      if (!it.next(l.t)) return false;
-      l.page = l.slot = 0;
+      if (!it.next()) return false;
+      l.keys = it.keys();
+      l.head = it.s.hv / p.blocks;
+      l.slot = it.slot;
+      l.page = 0;
       cp_async_wait<kAhead - 1>();
-      if (busy && row < l.t.n) {
-        l.slot = (l.t.pos + row) % p.page;
+      if (deals && row < l.keys) {
         l.page = static_cast<int>(ld_shared_u32(mine_p + stage * 128));
+        if (l.page < 0 || l.page >= p.pages) atomicCAS(p.status, 0u, kDevBadPage);  // TMA reads zeros there
       }
-      prefetch(stage);
-      stage = stage + 1 == kAhead ? 0 : stage + 1;
+      prefetch();
       return true;
     };
-    auto fill = [&](const Load &l, const CUtensorMap *tm) {
-      if (l.page < 0 || l.page >= p.pages) atomicCAS(p.status, 0u, kDevBadPage);  // TMA reads zeros there
-      const bool mine = busy && row < l.t.n;
-      const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, mine)) * rows) * 128u;
-      const int head = l.t.hv / p.blocks;
-      bool got = true;
-      for (int c = 0; c < C::NC; ++c) {
+    auto fill = [&](const Load &l, const CUtensorMap *tm, bool deal, int first) {
+      // boxes of this producer in the tile: lanes first, first + kProducers, ... below the used ones
+      const int used = (l.keys + rows - 1) / rows * C::NBOX;
+      const uint32_t bytes = used > first ? static_cast<uint32_t>((used - first + kProducers - 1) / kProducers * rows) * 128u : 0u;
+      for (int c = 0; ok && c < C::NC; ++c) {
         if (filled == C::NSLOT)
-          got = got && wait_bounded(BAR(C::B_EMPTY + slot), lap ^ 1u, &misc.abort_flag, p.status, kDevTimeoutLoad, p.wait_limit);
+          ok = wait_bounded(BAR(C::B_EMPTY + slot), lap ^ 1u, &misc.abort_flag, p.status, kDevTimeoutLoad, p.wait_limit);
         else
           ++filled;
-        got = __all_sync(0xffffffffu, got);
-        if (!got) {
-          ok = false;
-          break;
-        }
+        if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(BAR(C::B_FULL + slot), bytes);
-        __syncwarp();
-        if (mine)
-          tma_load_4d(base + slot * C::SLOT_BYTES + box * C::BOX_BYTES + row * 128, tm, c * C::CW + box * 64, l.slot, head, l.page,
+        if (deal && row < l.keys)
+          tma_load_4d(base + slot * C::SLOT_BYTES + box * C::BOX_BYTES + row * 128, tm, c * C::CW + box * 64, l.slot, l.head, l.page,
                       BAR(C::B_FULL + slot));
         if (++slot == C::NSLOT) {
           slot = 0;
@@ -393,26 +393,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     };
-    auto query = [&](const Tile &t) {  // Q of a segment, before its first K
-      const int s = t.seg;
-      if (s >= 2)
-        ok = __all_sync(0xffffffffu, wait_bounded(BAR(C::B_QEMPTY + (s & 1)), ((s - 2) >> 1) & 1, &misc.abort_flag, p.status,
-                                                  kDevTimeoutLoad, p.wait_limit));
-      if (!ok || lane != 0 || which != 0) return;
+    const int first_k = which, first_v = (which + kProducers - lanes % kProducers) % kProducers;
+    auto query = [&]() {  // Q of a segment, before its first K
+      const int s = it.seg;
+      if (s >= 2) ok = wait_bounded(BAR(C::B_QEMPTY + (s & 1)), ((s - 2) >> 1) & 1, &misc.abort_flag, p.status, kDevTimeoutLoad, p.wait_limit);
+      if (!ok) return;
       queries = s + 1;
       const uint32_t bar = BAR(C::B_QFULL + (s & 1)), dst = base + C::OFF_Q + (s & 1) * C::Q_BYTES;
       mbar_arrive_expect_tx(bar, static_cast<uint32_t>(p.q_rows) * 128u * (D / 64));
-      const int head = (t.hv / p.blocks) * p.G + (t.hv % p.blocks) * NH;
-      for (int x = 0; x < D / 64; ++x) tma_load_3d(dst + x * C::NQ * 128, &tm_q, x * 64, head, t.b, bar);
+      const int head = (it.s.hv / p.blocks) * p.G + (it.s.hv % p.blocks) * NH;
+      for (int x = 0; x < D / 64; ++x) tma_load_3d(dst + x * C::NQ * 128, &tm_q, x * 64, head, it.s.b, bar);
     };
     Load v, k;
     bool have_v = false, have_k = look(k);
     while (ok && (have_k || have_v)) {
       if (have_k) {
-        if (k.t.first) query(k.t);
-        if (ok) fill(k, &tm_k);
+        if (which == kProducers - 1 && lane == 0 && it.first()) query();
+        if (ok) fill(k, &tm_k, deals_k, first_k);
       }
-      if (ok && have_v) fill(v, &tm_v);
+      if (ok && have_v) fill(v, &tm_v, deals_v, first_v);
       v = k;
       have_v = have_k;
       have_k = have_k && look(k);

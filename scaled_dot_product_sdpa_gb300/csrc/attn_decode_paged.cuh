@@ -44,6 +44,7 @@ struct PagedParams {
   int G, blocks;                       // query heads per key head; blocks of them
   int box_rows;                        // rows of a TMA box: a power of two <= 128 that divides the page
   int q_rows;                          // rows of a query box
+  int tile_pages, tile_slots;          // kPagedTile / page, kPagedTile % page
   bool bf16;
   float c2;                            // scale log2(e)
   void *o;                             // [B, Hq, d]

@@ -419,6 +419,8 @@ extern "C" int attn_decode_paged(const void *q, long long q_sb, long long q_sh, 
   p.box_rows = std::min(page & -page, kPagedTile);
   const int rows_at_once = paged_heads(p.G, d);
   p.q_rows = std::min(rows_at_once, p.G);
+  p.tile_pages = kPagedTile / page;
+  p.tile_slots = kPagedTile % page;
   p.bf16 = dtype == GBATTN_BF16;
   p.c2 = scale * 1.4426950408889634f;
   p.o = o;
