@@ -46,10 +46,12 @@ struct PagedCfg {
   static constexpr int Q_BYTES = NQ * D * 2;
   static constexpr int NP = 2 * NH;                     // columns of P^T: hi parts, then lo parts
   static constexpr int P_BYTES = NP * kPagedTile * 2;
-  static constexpr int RED_BYTES = 3 * 4 * NH * 4;      // warps' maxima (two tiles) and sums
+  static constexpr int NQB = NH == 8 && D <= 128 ? 4 : NH == 32 && D == 256 ? 1 : 2;  // query buffers: segments looked ahead
+  // floats: warps' maxima of two tiles, their sums of two segments, the maxima of two segments
+  static constexpr int RED_SUMS = 8 * NH, RED_TOPS = 16 * NH, RED_BYTES = 18 * NH * 4;
   static constexpr int PAGE_BYTES = kProducers * kAhead * 32 * 4;  // page numbers read ahead, per producer lane
   static constexpr int BAR_BYTES = 512;                 // barriers and a few words
-  static constexpr int ROOM = 232448 - 1024 - 2 * Q_BYTES - 2 * P_BYTES - RED_BYTES - PAGE_BYTES - BAR_BYTES;
+  static constexpr int ROOM = 232448 - 1024 - NQB * Q_BYTES - 2 * P_BYTES - RED_BYTES - PAGE_BYTES - BAR_BYTES;
   static constexpr int FIT = ROOM / SLOT_BYTES, MOST = 196608 / SLOT_BYTES;
   static constexpr int NSLOT = FIT < MOST ? FIT : MOST;
   // With one slot a tile, the commit that frees K's slot also tells that S is there, and the one that
@@ -59,18 +61,18 @@ struct PagedCfg {
   static_assert(!ONE || NSLOT >= 5, "slots that the softmax waits on");
   static_assert(NSLOT > NC, "a tile's V slots are resident together while the next K slots pass");
   static constexpr int OFF_Q = NSLOT * SLOT_BYTES;
-  static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;
+  static constexpr int OFF_P = OFF_Q + NQB * Q_BYTES;
   static constexpr int OFF_RED = OFF_P + 2 * P_BYTES;
   static constexpr int OFF_PAGES = OFF_RED + RED_BYTES;
   static constexpr int OFF_BAR = OFF_PAGES + PAGE_BYTES;
   // barriers
-  static constexpr int B_FULL = 0, B_EMPTY = NSLOT, B_QFULL = 2 * NSLOT, B_QEMPTY = B_QFULL + 2, B_SFULL = B_QEMPTY + 2,
+  static constexpr int B_FULL = 0, B_EMPTY = NSLOT, B_QFULL = 2 * NSLOT, B_QEMPTY = B_QFULL + NQB, B_SFULL = B_QEMPTY + NQB,
                        B_PFULL = B_SFULL + 2, B_PDONE = B_PFULL + 2, B_DRAIN = B_PDONE + 2, NBAR = B_DRAIN + 1;
   static constexpr int SMEM_BYTES = 1024 + OFF_BAR + BAR_BYTES;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
   static constexpr int NO = D <= 128 ? 1 : D / 128;     // 128-column blocks of O
-  static constexpr int T_O = 2 * NQ;                    // TMEM columns: S twice, then O
-  static constexpr int T_USED = T_O + NO * NP;
+  static constexpr int T_O = 2 * NQ;                    // TMEM columns: S twice, then O twice
+  static constexpr int T_USED = T_O + 2 * NO * NP;       // O of two segments
   static constexpr int T_COLS = T_USED <= 64 ? 64 : T_USED <= 128 ? 128 : T_USED <= 256 ? 256 : 512;
   static_assert(T_USED <= 512, "tensor memory");
 };
@@ -115,6 +117,29 @@ __device__ __forceinline__ void split_weights(float a, float b, uint32_t &hi, ui
   lo = pack2<BF>(a - x, b - y);
 }
 
+// out[h] = the sum of l[h] over the warp: lanes halve the heads that they hold as they exchange.
+template <int NH>
+__device__ __forceinline__ void warp_sums(const float (&l)[NH], float *out) {
+  const int lane = threadIdx.x & 31;
+  float v[NH];
+#pragma unroll
+  for (int h = 0; h < NH; ++h) v[h] = l[h];
+  int off = 16;
+#pragma unroll
+  for (int n = NH / 2; n >= 1; n >>= 1, off >>= 1) {
+    const bool up = (lane & off) != 0;
+#pragma unroll
+    for (int k = 0; k < n; ++k) {
+      const float give = up ? v[k] : v[k + n], keep = up ? v[k + n] : v[k];
+      v[k] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+    }
+  }
+#pragma unroll
+  for (; off >= 1; off >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+  constexpr int per = 32 / NH;  // lanes that hold the same head
+  if ((lane & (per - 1)) == 0) out[lane / per] = v[0];
+}
+
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 // Tokens of sequence b, a bad length clamped into [0, table's end].
@@ -129,10 +154,10 @@ struct Seg {
   int b, hv, len, tile, count, tiles;  // tiles: of the whole row
 };
 
-// A row's place: sequence and offset of a CTA's first unit in it, and the share's units.
+// A CTA's share: its first unit's sequence (and that one's length), key head and tile, and its units.
 struct Start {
-  int b;
-  long long off, units;
+  int b, len, hv, tile;
+  long long units;
 };
 
 // Walks over a CTA's share.  By a warp, whose lanes hold 32 lengths at a time, or by one thread,
@@ -146,21 +171,20 @@ struct Walk {
     hvs = pp.Hkv * pp.blocks;
     b = base = at.b;
     left = at.units;
+    hv = at.hv;
+    tile = at.tile;
     if (left <= 0) return;
-    fetch();
-    const int nt = tiles_of(length());
-    hv = static_cast<int>(at.off / nt);
-    tile = static_cast<int>(at.off - static_cast<long long>(hv) * nt);
+    if constexpr (WARP) {
+      fetch();
+    } else {
+      len = at.len;
+      ahead = load(b + 1);
+    }
   }
   __device__ int load(int i) const { return i < p.B ? clamp_length(p.lengths[i], p) : 0; }
   __device__ void fetch() {
     base = b;
-    if constexpr (WARP) {
-      len = load(b + static_cast<int>(threadIdx.x & 31));
-    } else {
-      len = load(b);
-      ahead = load(b + 1);
-    }
+    len = load(b + static_cast<int>(threadIdx.x & 31));
   }
   __device__ int length() const {
     if constexpr (WARP) return __shfl_sync(0xffffffffu, len, b - base);
@@ -240,8 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = PagedCfg<D, NH>;
   extern __shared__ uint8_t smem_raw[];
   struct Misc {
-    long long warp_tiles[kThreads / 32], start_off;
-    int start_b;
+    long long warp_tiles[kThreads / 32];
+    Start start;
     uint32_t tmem_base;
     volatile uint32_t abort_flag;
   };
@@ -260,17 +284,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(BAR(C::B_FULL + i), kProducers);
       mbar_init(BAR(C::B_EMPTY + i), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::NQB; ++i) {
       mbar_init(BAR(C::B_QFULL + i), 1);
       mbar_init(BAR(C::B_QEMPTY + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(BAR(C::B_SFULL + i), 1);
       mbar_init(BAR(C::B_PFULL + i), 4);
       mbar_init(BAR(C::B_PDONE + i), 1);
     }
     mbar_init(BAR(C::B_DRAIN), 1);
     misc.abort_flag = 0u;
-    misc.start_b = 0;
-    misc.start_off = 0;
+    misc.start = {0, 0, 0, 0, 0};
     fence_mbar_init();
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
@@ -290,8 +315,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int per = (p.B + kThreads - 1) / kThreads;
   const int s0 = min(p.B, tid * per), s1 = min(p.B, s0 + per);
   long long mine = 0;
+  int len0 = 0;  // of its first sequence
   for (int b = s0; b < s1; ++b) {
     const int n = p.lengths[b], m = clamp_length(n, p);
+    if (b == s0) len0 = m;
     if (n != m && blockIdx.x == 0) atomicCAS(p.status, 0u, kDevBadLength);
     mine += static_cast<long long>(tiles_of(m)) * hvs;
   }
@@ -314,22 +341,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long u0 = total * cta / G, u1 = total * min(cta + 1, G) / G;
   if (u0 < u1 && upto - mine <= u0 && u0 < upto) {
     long long off = u0 - (upto - mine);
-    for (int b = s0; b < s1; ++b) {
-      const long long units = static_cast<long long>(tiles_of(clamp_length(p.lengths[b], p))) * hvs;
-      if (off < units) {
-        misc.start_b = b;
-        misc.start_off = off;
-        break;
-      }
+    int b = s0, n = len0;
+    for (;; n = clamp_length(p.lengths[++b], p)) {  // ends before s1: the run holds unit u0
+      const long long units = static_cast<long long>(tiles_of(n)) * hvs;
+      if (off < units) break;
       off -= units;
     }
+    const unsigned long long nt = static_cast<unsigned long long>(tiles_of(n)), o = static_cast<unsigned long long>(off);
+    // 32-bit division where it serves (it nearly always does)
+    const unsigned long long hv = (o >> 32) == 0 ? static_cast<uint32_t>(o) / static_cast<uint32_t>(nt) : o / nt;
+    misc.start = {b, n, static_cast<int>(hv), static_cast<int>(o - hv * nt), u1 - u0};
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc.tmem_base;
   const long long T = u1 - u0;
-  const Start start = {misc.start_b, misc.start_off, T};
+  const Start start = misc.start;
   bool ok = true;
 
   if (warp >= 5) {
@@ -396,10 +424,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int first_k = which, first_v = (which + kProducers - lanes % kProducers) % kProducers;
     auto query = [&]() {  // Q of a segment, before its first K
       const int s = it.seg;
-      if (s >= 2) ok = wait_bounded(BAR(C::B_QEMPTY + (s & 1)), ((s - 2) >> 1) & 1, &misc.abort_flag, p.status, kDevTimeoutLoad, p.wait_limit);
+      if (s >= C::NQB) ok = wait_bounded(BAR(C::B_QEMPTY + s % C::NQB), (s / C::NQB - 1) & 1, &misc.abort_flag, p.status, kDevTimeoutLoad, p.wait_limit);
       if (!ok) return;
       queries = s + 1;
-      const uint32_t bar = BAR(C::B_QFULL + (s & 1)), dst = base + C::OFF_Q + (s & 1) * C::Q_BYTES;
+      const uint32_t bar = BAR(C::B_QFULL + s % C::NQB), dst = base + C::OFF_Q + (s % C::NQB) * C::Q_BYTES;
       mbar_arrive_expect_tx(bar, static_cast<uint32_t>(p.q_rows) * 128u * (D / 64));
       const int head = (it.s.hv / p.blocks) * p.G + (it.s.hv % p.blocks) * NH;
       for (int x = 0; x < D / 64; ++x) tma_load_3d(dst + x * C::NQ * 128, &tm_q, x * 64, head, it.s.b, bar);
@@ -422,7 +450,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // and gets some milliseconds).
     if (lane == 0 && misc.abort_flag) {
       for (uint32_t x = 0; x < filled; ++x) wait_drain(BAR(C::B_FULL + x), x < slot ? lap : lap ^ 1u, p.wait_limit >> 10);
-      for (int x = max(0, queries - 2); x < queries; ++x) wait_drain(BAR(C::B_QFULL + (x & 1)), (x >> 1) & 1, p.wait_limit >> 10);
+      for (int x = max(0, queries - C::NQB); x < queries; ++x)
+        wait_drain(BAR(C::B_QFULL + x % C::NQB), (x / C::NQB) & 1, p.wait_limit >> 10);
     }
     __syncwarp();
   } else if (warp == 4) {
@@ -449,8 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       auto qk = [&](uint32_t i, uint32_t seg, bool first, bool last) {
-        const uint32_t buf = i & 1u, qb = seg & 1u;
-        if (first) wait(C::B_QFULL + qb, seg >> 1);
+        const uint32_t buf = i & 1u, qb = seg % C::NQB;
+        if (first) wait(C::B_QFULL + qb, seg / C::NQB);
         // S(i - 2) has been read: PV(i - 2), issued before, waited for the weights made of it.
         for (int c = 0; c < C::NC; ++c, step()) {
           wait(C::B_FULL + slot, lap);
@@ -468,8 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (last) umma_commit(BAR(C::B_QEMPTY + qb));
         }
       };
-      auto pv = [&](uint32_t i, bool first) {
-        const uint32_t buf = i & 1u;
+      auto pv = [&](uint32_t i, uint32_t seg, bool first) {
+        const uint32_t buf = i & 1u, o = tmem + C::T_O + (seg & 1u) * (C::NO * C::NP);
         wait(C::B_PFULL + buf, i >> 1);
         for (int c = 0; c < C::NC; ++c, step()) {
           wait(C::B_FULL + slot, lap);
@@ -477,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < kPagedTile / 16; ++kk)
-              umma_ss_off(tmem + C::T_O + c * C::NP, dv, slot * C::SLOT_BYTES + kk * 2048, dp, buf * C::P_BYTES + kk * (16 * 4 * NH), idesc_o,
+              umma_ss_off(o + c * C::NP, dv, slot * C::SLOT_BYTES + kk * 2048, dp, buf * C::P_BYTES + kk * (16 * 4 * NH), idesc_o,
                           !first || kk > 0);
             umma_commit(BAR(C::B_EMPTY + slot));
           }
@@ -489,16 +518,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       Seg s;
       uint32_t i = 0, seg = 0;
       bool pending = false, pending_first = false;  // PV(i - 1) is due
+      uint32_t pending_seg = 0;
       while (got && w.next(s)) {
         for (int j = 0; got && j < s.count; ++j, ++i) {
           qk(i, seg, j == 0, j == s.count - 1);
-          if (got && pending) pv(i - 1, pending_first);
+          if (got && pending) pv(i - 1, pending_seg, pending_first);
           pending = true;
           pending_first = j == 0;
+          pending_seg = seg;
         }
         ++seg;
       }
-      if (got && pending) pv(i - 1, pending_first);
+      if (got && pending) pv(i - 1, pending_seg, pending_first);
       if (misc.abort_flag) {  // after a time-out: products in flight end before the CTA does
         umma_commit(BAR(C::B_DRAIN));
         wait_drain(BAR(C::B_DRAIN), 0, p.wait_limit);
@@ -534,11 +565,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       else
         wait(C::B_PDONE + static_cast<int>(t & 1), t >> 1);
     };
+    // A segment's results wait for its last PV; they are taken after the next segment's first tile.
+    struct {
+      int heads = 0;  // 0: none due
+      bool whole, begins;
+      uint32_t last, seg;
+      size_t row0;
+    } due;
+    auto results = [&]() {
+      wait_pv(due.last);
+      tc_fence_after();
+      const size_t part = 2 * static_cast<size_t>(blockIdx.x) + (due.begins ? 1 : 0);
+      const float *const sums = red + C::RED_SUMS + (due.seg & 1) * 4 * NH, *const tops = red + C::RED_TOPS + (due.seg & 1) * NH;
+      const uint32_t from = lanes + C::T_O + (due.seg & 1) * (C::NO * C::NP);
+      float inv[NH];
+#pragma unroll
+      for (int g = 0; g < NH; g += 4)
+        if (g < due.heads) {
+          const float4 *const r = reinterpret_cast<const float4 *>(sums + g);
+          const float4 a = r[0], b = r[NH / 4], c = r[2 * NH / 4], d = r[3 * NH / 4];
+          const float t[4] = {(a.x + b.x) + (c.x + d.x), (a.y + b.y) + (c.y + d.y), (a.z + b.z) + (c.z + d.z), (a.w + b.w) + (c.w + d.w)};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) inv[g + e] = t[e] == 0.f ? 0.f : 1.f / t[e];
+        }
+      if (ok && tid < due.heads) {
+        const float lse2 = tops[tid] - kShift + __log2f((sums[tid] + sums[NH + tid]) + (sums[2 * NH + tid] + sums[3 * NH + tid]));
+        if (due.whole)
+          p.lse[due.row0 + tid] = lse2 * 0.69314718055994531f;
+        else
+          p.part_lse[part * NH + tid] = lse2;
+      }
+#pragma unroll
+      for (int ob = 0; ob < C::NO; ++ob) {
+        uint32_t o[C::NP];
+        tmem_ld<C::NP>(from + ob * C::NP, o);
+        const int col = ob * 128 + tid;
+        if (ok && (D >= 128 || tid < D))
+#pragma unroll
+          for (int h = 0; h < NH; ++h)
+            if (h < due.heads) {
+              const float y = (__uint_as_float(o[h]) + __uint_as_float(o[NH + h])) * inv[h];
+              if (!due.whole)
+                p.part_o[(part * NH + h) * D + col] = y;
+              else if (p.bf16)
+                static_cast<__nv_bfloat16 *>(p.o)[(due.row0 + h) * D + col] = __float2bfloat16_rn(y);
+              else
+                static_cast<__half *>(p.o)[(due.row0 + h) * D + col] = __float2half_rn(y);
+            }
+      }
+      tc_fence_before();
+      due.heads = 0;
+    };
     Walk<true> w(p, start);
     Seg s;
     uint32_t i = 0;  // tiles done
-    while (w.next(s)) {
+    for (uint32_t seg = 0; w.next(s); ++seg) {
       const int block = s.hv % p.blocks, heads = min(NH, p.G - block * NH);
+      const uint32_t o_at = lanes + C::T_O + (seg & 1) * (C::NO * C::NP);
       float m[NH], l[NH];
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
@@ -633,13 +716,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int ob = 0; ob < C::NO; ++ob) {
               uint32_t o[C::NP];
-              tmem_ld<C::NP>(lanes + C::T_O + ob * C::NP, o);
+              tmem_ld<C::NP>(o_at + ob * C::NP, o);
 #pragma unroll
               for (int h = 0; h < NH; ++h) {
                 o[h] = __float_as_uint(__uint_as_float(o[h]) * keep[h]);
                 o[NH + h] = __float_as_uint(__uint_as_float(o[NH + h]) * keep[h]);
               }
-              tmem_st<C::NP>(lanes + C::T_O + ob * C::NP, o);
+              tmem_st<C::NP>(o_at + ob * C::NP, o);
             }
           }
         }
@@ -666,68 +749,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(C::B_PFULL + buf));
+        if (due.heads) results();  // of the segment before
       }
-      // ---------------------------------------------------------- the segment's results
-      float *const sums = red + 8 * NH;
+      // ---------------------------------------------------------- the segment's sums
+      // (the next barrier, of the next tile or the last one, makes them visible)
+      warp_sums<NH>(l, red + C::RED_SUMS + ((seg & 1) * 4 + warp) * NH);
+      if (tid == 0) {
+        float *const tops = red + C::RED_TOPS + (seg & 1) * NH;
 #pragma unroll
-      for (int h = 0; h < NH; ++h)
-        if (h < heads) {
-          float t = l[h];
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-          if (lane == 0) sums[warp * NH + h] = t;
-        }
-      softmax_sync();
-      wait_pv(i - 1);
-      tc_fence_after();
-      const bool whole = s.count == s.tiles, begins = s.tile == 0;
-      const int head0 = (s.hv / p.blocks) * p.G + block * NH;
-      const size_t row0 = static_cast<size_t>(s.b) * p.Hq + head0;
-      const size_t part = 2 * static_cast<size_t>(blockIdx.x) + (begins ? 1 : 0);
-      float inv[NH];
-#pragma unroll
-      for (int h = 0; h < NH; ++h)
-        if (h < heads) {
-          const float t = sums[h] + sums[NH + h] + (sums[2 * NH + h] + sums[3 * NH + h]);
-          inv[h] = t == 0.f ? 0.f : 1.f / t;
-          if (ok && tid == h) {
-            const float lse2 = m[h] - kShift + __log2f(t);
-            if (whole)
-              p.lse[row0 + h] = lse2 * 0.69314718055994531f;
-            else
-              p.part_lse[part * NH + h] = lse2;
-          }
-        }
-#pragma unroll
-      for (int ob = 0; ob < C::NO; ++ob) {
-        uint32_t o[C::NP];
-        tmem_ld<C::NP>(lanes + C::T_O + ob * C::NP, o);
-        const int col = ob * 128 + tid;
-        if (ok && (D >= 128 || tid < D))
-#pragma unroll
-          for (int h = 0; h < NH; ++h)
-            if (h < heads) {
-              const float y = (__uint_as_float(o[h]) + __uint_as_float(o[NH + h])) * inv[h];
-              if (!whole)
-                p.part_o[(part * NH + h) * D + col] = y;
-              else if (p.bf16)
-                static_cast<__nv_bfloat16 *>(p.o)[(row0 + h) * D + col] = __float2bfloat16_rn(y);
-              else
-                static_cast<__half *>(p.o)[(row0 + h) * D + col] = __float2half_rn(y);
-            }
+        for (int h = 0; h < NH; h += 4) *reinterpret_cast<float4 *>(tops + h) = make_float4(m[h], m[h + 1], m[h + 2], m[h + 3]);
       }
-      tc_fence_before();
-      if (!whole && begins) {
-        // The row goes on in the next CTAs: up to the one whose share holds its last unit.
+      due.heads = heads;
+      due.whole = s.count == s.tiles;
+      due.begins = s.tile == 0;
+      due.last = i - 1;
+      due.seg = seg;
+      due.row0 = static_cast<size_t>(s.b) * p.Hq + (s.hv / p.blocks) * p.G + block * NH;
+      if (!due.whole && due.begins) {
+        // The row goes on in the next CTAs: up to the one whose share holds its last unit `end`, the
+        // largest c with floor(total c / G) <= end, that is c < (end + 1) G / total.
         const long long end = u1 + (s.tiles - s.count) - 1;
-        long long c = end * G / total;
-        while (total * (c + 1) / G <= end) ++c;
-        while (total * c / G > end) --c;
-        record.head = static_cast<int>(row0);
+        record.head = static_cast<int>(due.row0);
         record.heads = heads;
-        record.parts = static_cast<int>(c) - static_cast<int>(blockIdx.x) + 1;
+        record.parts = static_cast<int>(((end + 1) * G - 1) / total) - static_cast<int>(blockIdx.x) + 1;
       }
     }
+    softmax_sync();
+    if (due.heads) results();
     if (tid == 0 && p.records) p.records[blockIdx.x] = record;
   }
   tc_fence_before();

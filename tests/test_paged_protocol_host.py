@@ -37,12 +37,7 @@ def shares(lengths, hvs, G):
             row, first, n, whole = segs[-1]
             if first == 0 and n < whole:
                 end = u1 + (whole - n) - 1
-                d = end * G // total
-                while total * (d + 1) // G <= end:
-                    d += 1
-                while total * d // G > end:
-                    d -= 1
-                record = d - c + 1
+                record = ((end + 1) * G - 1) // total - c + 1
         out.append((segs, record))
     return out
 
@@ -79,9 +74,9 @@ def v_pos(t, T, nc):
     return (min(t + 2, T) + t) * nc
 
 
-@pytest.mark.parametrize("nc,nslot", [(1, 12), (1, 5), (2, 6), (2, 5), (4, 6), (4, 5)])
+@pytest.mark.parametrize("nc,nslot,nqb", [(1, 12, 4), (1, 6, 4), (1, 5, 2), (2, 6, 2), (2, 5, 2), (2, 4, 1), (4, 6, 2), (4, 5, 2)])
 @pytest.mark.parametrize("seed", range(40))
-def test_ring_protocol(nc, nslot, seed):
+def test_ring_protocol(nc, nslot, nqb, seed):
     """The three roles step by step in a random interleaving, each blocked exactly where the kernel waits.  Loads, products and
     arrivals complete at once or later, at random."""
     rng = random.Random(seed)
@@ -102,8 +97,8 @@ def test_ring_protocol(nc, nslot, seed):
     def arrive(bar):
         done[bar] = done.get(bar, 0) + 1
 
-    slots, s_buf, p_buf, q_buf = [None] * nslot, [None] * 2, [None] * 2, [None] * 2
-    order, read = [], set()
+    slots, s_buf, p_buf, q_buf = [None] * nslot, [None] * 2, [None] * 2, [None] * nqb
+    order, read, o_buf = [], set(), [None] * 2
 
     def producer():
         at = 0
@@ -113,10 +108,10 @@ def test_ring_protocol(nc, nslot, seed):
                     continue
                 if what == "K" and first[u]:
                     s = seg[u]
-                    while s >= 2 and not ready(("qempty", s & 1), (s - 2) >> 1):
+                    while s >= nqb and not ready(("qempty", s % nqb), s // nqb - 1):
                         yield
-                    q_buf[s & 1] = s
-                    arrive(("qfull", s & 1))
+                    q_buf[s % nqb] = s
+                    arrive(("qfull", s % nqb))
                 if what == "V":
                     assert at == v_pos(u, T, nc)
                 for c in range(nc):
@@ -145,15 +140,15 @@ def test_ring_protocol(nc, nslot, seed):
                 yield
 
         def qk(t):
-            while first[t] and not ready(("qfull", seg[t] & 1), seg[t] >> 1):
+            while first[t] and not ready(("qfull", seg[t] % nqb), seg[t] // nqb):
                 yield
             assert t < 2 or t - 2 in read, "S is rewritten before it was read"
-            assert q_buf[seg[t] & 1] == seg[t]
+            assert q_buf[seg[t] % nqb] == seg[t]
             yield from take("K", t, lambda: s_buf.__setitem__(t & 1, t))
             if nc > 1:
                 arrive(("sfull", t & 1))
             if last[t]:
-                arrive(("qempty", seg[t] & 1))
+                arrive(("qempty", seg[t] % nqb))
 
         yield from qk(0)
         for t in range(T):
@@ -162,6 +157,8 @@ def test_ring_protocol(nc, nslot, seed):
             while not ready(("pfull", t & 1), t >> 1):
                 yield
             assert p_buf[t & 1] == t
+            assert not first[t] or o_buf[seg[t] & 1] is None, "O is overwritten before its results were taken"
+            o_buf[seg[t] & 1] = seg[t]
             yield from take("V", t, lambda: order.append(t))
             if nc > 1:
                 arrive(("pdone", t & 1))
@@ -174,7 +171,15 @@ def test_ring_protocol(nc, nslot, seed):
         x = v_pos(t, T, 1)
         return ready(("empty", x % nslot), x // nslot) if nc == 1 else ready(("pdone", t & 1), t >> 1)
 
+    def results(t):
+        """Of the segment that ends with tile t, taken a tile later."""
+        while not pv_done(t):
+            yield
+        assert order[:t + 1] == list(range(t + 1)) and o_buf[seg[t] & 1] == seg[t]
+        o_buf[seg[t] & 1] = None
+
     def softmax():
+        due = None
         for t in range(T):
             while not s_there(t):
                 yield
@@ -200,11 +205,11 @@ def test_ring_protocol(nc, nslot, seed):
                     assert slots[x % nslot] == ("V", t, c)
                     yield
             arrive(("pfull", t & 1))
-            if last[t]:
-                while not pv_done(t):
-                    yield
-                assert order == list(range(t + 1))
+            if due is not None:
+                yield from results(due)
+            due = t if last[t] else None
             yield
+        yield from results(due)
 
     roles = [producer(), mma(), softmax()]
     idle = 0
