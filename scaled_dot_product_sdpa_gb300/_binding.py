@@ -358,11 +358,15 @@ def attn_fwd_host(q, k, v, causal: bool = False, scale: float | None = None, o=N
 # ---------------------------------------------------------------------------------------
 # Rotary positions and the paged cache.  Tensors of a call share one device and, but for the
 # integer and frequency tensors, one type (float16 or bfloat16).  What a call allocates
-# belongs to the stream that it runs on.
+# belongs to the stream that it runs on.  A decoding step makes several of these calls, each
+# worth a few microseconds on the GPU, so the checks read each property of a tensor once.
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+_current_stream = torch._C._cuda_getCurrentRawStream  # of a device index; torch.cuda.current_stream costs 3 us
 
 
-def _empty(shape, dtype, device, stream):
+def _empty(shape, dtype, like, stream):
+    """An uninitialised tensor on the device of `like` that belongs to `stream`."""
+    device = like.device
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     if not hasattr(stream, "cuda_stream"):
@@ -371,94 +375,117 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _launch(what, fn, device, stream, *args):
-    """Call the C entry point `fn` with the device current and its stream as last argument."""
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, _stream_handle(stream))
+def _launch(what, fn, dev, stream, *args):
+    """Call the C entry point `fn` with device `dev` current and its stream as last argument."""
+    handle = _current_stream(dev) if stream is None else _stream_handle(stream)
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, handle)
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, _stream_handle(stream))
+        with torch.cuda.device(dev):
+            rc = fn(*args, handle)
     if rc != 0:
         raise GbattnError(rc, what)
 
 
-def _check_like(t, name, q, shape=None):
-    if not t.is_cuda or t.device != q.device:
-        raise ValueError(f"gbattn: {name} must be on the CUDA device of the other tensors (no CPU path exists)")
-    if t.dtype != q.dtype:
-        raise ValueError(f"gbattn: {name} must be {q.dtype} like the other tensors")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"gbattn: {name} must have the shape {tuple(shape)}")
-
-
-def _dtype_code(t, name):
-    if not t.is_cuda:
+def _device_and_type(t, name):
+    """Device index and type code of a call's first tensor."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("gbattn: tensors must be on a CUDA device (no CPU path exists)")
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise ValueError(f"gbattn: {name} must be float16 or bfloat16")
-    return code
+    return dev, code
 
 
-def _rows(t, name):
-    """(pointer, strides of batch, head and row) of [B, H, L, d] rows; the last dimension must be
+def _check_like(t, name, dev, dtype):
+    if t.get_device() != dev:
+        raise ValueError(f"gbattn: {name} must be on the CUDA device of the other tensors (no CPU path exists)")
+    if t.dtype != dtype:
+        raise ValueError(f"gbattn: {name} must be {dtype} like the other tensors")
+
+
+def _rows(t, name, shape):
+    """Pointer and strides of batch, head and row of [B, H, L, d] rows; the last dimension must be
     contiguous, the strides of dimensions of one element do not matter."""
     sb, sh, sl, sd = t.stride()
-    B, H, L, _ = t.shape
     if sd != 1:
         raise ValueError(f"gbattn: the last dimension of {name} must be contiguous")
-    return t.data_ptr(), sb if B > 1 else 0, sh if H > 1 else 0, sl if L > 1 else 0
+    B, H, L, _ = shape
+    return t.data_ptr(), (sb if B > 1 else 0), (sh if H > 1 else 0), (sl if L > 1 else 0)
 
 
 _NO_ROWS = (None, 0, 0, 0)
 
 
-def _out(t, name, shape, dtype, like, stream):
-    if t is None:
-        return _empty(shape, dtype, like.device, stream)
-    if t.shape != shape or t.dtype != dtype or t.device != like.device or not t.is_contiguous():
+def _check_out(t, name, shape, dtype, dev):
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"gbattn: {name} must be contiguous {dtype} {tuple(shape)} on the device of the other tensors")
     return t
 
 
-def _ints(t, name, shape, like):
-    """(pointer, row stride) of an int32 device tensor whose last dimension is contiguous."""
-    if t.dtype != torch.int32 or t.device != like.device or t.shape != shape:
-        raise ValueError(f"gbattn: {name} must be int32 {tuple(shape)} on the device of the other tensors")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+def _ints(t, name, n, dev):
+    """Pointer of an int32 [n] device tensor."""
+    if t.dtype != torch.int32 or t.get_device() != dev or t.shape != (n,):
+        raise ValueError(f"gbattn: {name} must be int32 {(n,)} on the device of the other tensors")
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"gbattn: {name} must be contiguous")
+    return t.data_ptr()
+
+
+def _int_rows(t, name, B, dev, width=None):
+    """Pointer, row stride and width of an int32 [B, width] device tensor with contiguous rows."""
+    shape = t.shape
+    if t.dtype != torch.int32 or t.get_device() != dev or len(shape) != 2 or shape[0] != B or (width is not None and shape[1] != width):
+        raise ValueError(f"gbattn: {name} must be int32 [{B}, {'width' if width is None else width}] on the device of the other tensors")
+    sr, sc = t.stride()
+    if sc != 1 and shape[1] > 1:
         raise ValueError(f"gbattn: the last dimension of {name} must be contiguous")
-    return t.data_ptr(), (t.stride(0) if t.dim() == 2 and t.shape[0] > 1 else 0)
+    return t.data_ptr(), (sr if B > 1 else 0), shape[1]
 
 
-def _frequencies(inv_freq, d, like):
-    """(pointer, rotary width) of the inverse frequencies (None: nothing is rotated)."""
+def _frequencies(inv_freq, dev):
+    """Pointer and rotary width of the inverse frequencies (None: nothing is rotated)."""
     if inv_freq is None:
         return None, 0
-    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or inv_freq.device != like.device or not inv_freq.is_contiguous():
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or inv_freq.get_device() != dev or not inv_freq.is_contiguous():
         raise ValueError("gbattn: inv_freq must be contiguous float64 [rotary / 2] on the device of the other tensors")
     n = 2 * inv_freq.shape[0]
     return (inv_freq.data_ptr() if n else None), n
 
 
-def _norm_weights(q_weight, k_weight, d, q, has_q, has_k):
+def _weight(t, name, d, dev, dtype):
+    _check_like(t, name, dev, dtype)
+    if t.shape != (d,) or not t.is_contiguous():
+        raise ValueError(f"gbattn: {name} must be contiguous [{d}]")
+    return t.data_ptr()
+
+
+def _norm_weights(q_weight, k_weight, d, dev, dtype, has_q, has_k):
     if q_weight is None and k_weight is None:
         return None, None
     if (q_weight is None) == has_q or (k_weight is None) == has_k:
         raise ValueError("gbattn: norms need a weight for each tensor that is normalised")
-    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None:
-            _check_like(t, name, q, (d,))
-            if not t.is_contiguous():
-                raise ValueError(f"gbattn: {name} must be contiguous")
-    return q_weight.data_ptr() if has_q else None, k_weight.data_ptr() if has_k else None
+    return (_weight(q_weight, "q_weight", d, dev, dtype) if has_q else None,
+            _weight(k_weight, "k_weight", d, dev, dtype) if has_k else None)
 
 
-def _rope_positions(positions, B, L, like):
+def _rope_positions(positions, B, L, dev):
     if positions is None:
         return None, 0
     if positions.dim() == 1:
-        return _ints(positions, "positions", (L,), like)[0], 0
-    return _ints(positions, "positions", (B, L), like)
+        return _ints(positions, "positions", L, dev), 0
+    return _int_rows(positions, "positions", B, dev, L)[:2]
+
+
+def _workspace(workspace, nbytes, like, dev, stream):
+    if workspace is None:
+        return _empty(nbytes // 4, torch.float32, like, stream)
+    if (workspace.get_device() != dev or not workspace.is_contiguous()
+            or workspace.numel() * workspace.element_size() < nbytes):
+        raise ValueError(f"gbattn: workspace must be a contiguous CUDA tensor of at least {nbytes} bytes on the device "
+                         "of the other tensors")
+    return workspace
 
 
 def attn_rope(q, k, inv_freq, positions=None, interleaved: bool = False, factor: float = 1.0, q_weight=None,
@@ -470,27 +497,29 @@ def attn_rope(q, k, inv_freq, positions=None, interleaved: bool = False, factor:
     inv_freq: float64 [rotary / 2] (attn_rope_frequencies), rotary a multiple of 16 up to d;
     positions: int32 [B, L] or [L], default 0 .. L-1; interleaved: pairs (2r, 2r + 1) instead of
     (r, r + rotary / 2); factor multiplies cosine and sine.  Enqueued on `stream`."""
-    code = _dtype_code(q, "q")
-    if q.dim() != 4:
+    dev, code = _device_and_type(q, "q")
+    dtype, shape = q.dtype, q.shape
+    if len(shape) != 4:
         raise ValueError("gbattn: q must be [B, H, L, d]")
-    B, Hq, L, d = q.shape
-    Hkv = 0
-    kr = _NO_ROWS
+    B, Hq, L, d = shape
+    Hkv, kr, k_to = 0, _NO_ROWS, None
     if k is not None:
-        if k.dim() != 4 or k.shape[0] != B or k.shape[2] != L or k.shape[3] != d:
+        k_shape = k.shape
+        if len(k_shape) != 4 or k_shape[0] != B or k_shape[2] != L or k_shape[3] != d:
             raise ValueError("gbattn: k must be [B, Hkv, L, d] like q")
-        _check_like(k, "k", q)
-        Hkv = k.shape[1]
-        kr = _rows(k, "k")
-        k_out = _out(k_out, "k_out", k.shape, q.dtype, q, stream)
-    fp, rotary = _frequencies(inv_freq, d, q)
-    pp, ps = _rope_positions(positions, B, L, q)
-    wq, wk = _norm_weights(q_weight, k_weight, d, q, True, k is not None)
-    q_out = _out(q_out, "q_out", q.shape, q.dtype, q, stream)
-    _launch("attn_rope", load_library().attn_rope, q.device, stream, *_rows(q, "q"), *kr, q_out.data_ptr(),
-            k_out.data_ptr() if k is not None else None, fp, rotary, int(bool(interleaved)), float(factor), pp, ps, wq, wk,
-            float(eps), code, B, Hq, Hkv, L, d)
-    return q_out, (k_out if k is not None else None)
+        _check_like(k, "k", dev, dtype)
+        Hkv, kr = k_shape[1], _rows(k, "k", k_shape)
+        k_out = _empty(k_shape, dtype, q, stream) if k_out is None else _check_out(k_out, "k_out", k_shape, dtype, dev)
+        k_to = k_out.data_ptr()
+    else:
+        k_out = None
+    fp, rotary = _frequencies(inv_freq, dev)
+    pp, ps = _rope_positions(positions, B, L, dev)
+    wq, wk = _norm_weights(q_weight, k_weight, d, dev, dtype, True, k is not None)
+    q_out = _empty(shape, dtype, q, stream) if q_out is None else _check_out(q_out, "q_out", shape, dtype, dev)
+    _launch("attn_rope", (_lib or load_library()).attn_rope, dev, stream, *_rows(q, "q", shape), *kr, q_out.data_ptr(), k_to,
+            fp, rotary, bool(interleaved), factor, pp, ps, wq, wk, eps, code, B, Hq, Hkv, L, d)
+    return q_out, k_out
 
 
 def attn_rope_bwd(dq, dk, inv_freq, positions=None, interleaved: bool = False, factor: float = 1.0, q=None, k=None,
@@ -500,47 +529,53 @@ def attn_rope_bwd(dq, dk, inv_freq, positions=None, interleaved: bool = False, f
     results; dk None without keys) those of its inputs, contiguous: (dq_out, dk_out).  With norms, q and k
     are attn_rope's inputs and the result is (dq_out, dk_out, dq_weight, dk_weight), the weights'
     gradients in float32 [d].  The other arguments are attn_rope's."""
-    code = _dtype_code(dq, "dq")
-    if dq.dim() != 4:
+    dev, code = _device_and_type(dq, "dq")
+    dtype, shape = dq.dtype, dq.shape
+    if len(shape) != 4:
         raise ValueError("gbattn: dq must be [B, H, L, d]")
-    B, Hq, L, d = dq.shape
-    Hkv = 0
-    kr = _NO_ROWS
+    B, Hq, L, d = shape
+    Hkv, kr, k_to = 0, _NO_ROWS, None
     if dk is not None:
-        if dk.dim() != 4 or dk.shape[0] != B or dk.shape[2] != L or dk.shape[3] != d:
+        k_shape = dk.shape
+        if len(k_shape) != 4 or k_shape[0] != B or k_shape[2] != L or k_shape[3] != d:
             raise ValueError("gbattn: dk must be [B, Hkv, L, d] like dq")
-        _check_like(dk, "dk", dq)
-        Hkv = dk.shape[1]
-        kr = _rows(dk, "dk")
-        dk_out = _out(dk_out, "dk_out", dk.shape, dq.dtype, dq, stream)
-    fp, rotary = _frequencies(inv_freq, d, dq)
-    pp, ps = _rope_positions(positions, B, L, dq)
-    wq, wk = _norm_weights(q_weight, k_weight, d, dq, True, dk is not None)
-    lib = load_library()
+        _check_like(dk, "dk", dev, dtype)
+        Hkv, kr = k_shape[1], _rows(dk, "dk", k_shape)
+        dk_out = _empty(k_shape, dtype, dq, stream) if dk_out is None else _check_out(dk_out, "dk_out", k_shape, dtype, dev)
+        k_to = dk_out.data_ptr()
+    else:
+        dk_out = None
+    fp, rotary = _frequencies(inv_freq, dev)
+    pp, ps = _rope_positions(positions, B, L, dev)
+    wq, wk = _norm_weights(q_weight, k_weight, d, dev, dtype, True, dk is not None)
+    lib = _lib or load_library()
     xq = xk = _NO_ROWS
-    norm = wq is not None
-    if norm:
+    wq_to = wk_to = ws = None
+    if wq is not None:
         if q is None or (dk is not None) != (k is not None):
             raise ValueError("gbattn: the gradients of norms need attn_rope's inputs q and k")
-        _check_like(q, "q", dq, dq.shape)
-        xq = _rows(q, "q")
-        dq_weight = _out(dq_weight, "dq_weight", (d,), torch.float32, dq, stream)
+        _check_like(q, "q", dev, dtype)
+        if q.shape != shape or (k is not None and k.shape != k_shape):
+            raise ValueError("gbattn: q and k must have the shapes of dq and dk")
+        xq = _rows(q, "q", shape)
+        dq_weight = _empty(d, torch.float32, dq, stream) if dq_weight is None else _check_out(dq_weight, "dq_weight", (d,), torch.float32, dev)
+        wq_to = dq_weight.data_ptr()
         if k is not None:
-            _check_like(k, "k", dq, dk.shape)
-            xk = _rows(k, "k")
-            dk_weight = _out(dk_weight, "dk_weight", (d,), torch.float32, dq, stream)
+            _check_like(k, "k", dev, dtype)
+            xk = _rows(k, "k", k_shape)
+            dk_weight = _empty(d, torch.float32, dq, stream) if dk_weight is None else _check_out(dk_weight, "dk_weight", (d,), torch.float32, dev)
+            wk_to = dk_weight.data_ptr()
         nbytes = lib.attn_rope_bwd_workspace_bytes(d)
         if nbytes < 0:
             raise GbattnError(int(nbytes), "attn_rope_bwd_workspace_bytes")
-        workspace = _workspace(workspace, nbytes, dq, stream)
-    dq_out = _out(dq_out, "dq_out", dq.shape, dq.dtype, dq, stream)
-    _launch("attn_rope_bwd", lib.attn_rope_bwd, dq.device, stream, *_rows(dq, "dq"), *kr, *xq, *xk, dq_out.data_ptr(),
-            dk_out.data_ptr() if dk is not None else None, dq_weight.data_ptr() if norm else None,
-            dk_weight.data_ptr() if norm and dk is not None else None, fp, rotary, int(bool(interleaved)), float(factor), pp,
-            ps, wq, wk, float(eps), workspace.data_ptr() if norm else None, code, B, Hq, Hkv, L, d)
-    if dk is None:
-        dk_out = None
-    return (dq_out, dk_out, dq_weight, dk_weight if dk is not None else None) if norm else (dq_out, dk_out)
+        workspace = _workspace(workspace, nbytes, dq, dev, stream)
+        ws = workspace.data_ptr()
+    dq_out = _empty(shape, dtype, dq, stream) if dq_out is None else _check_out(dq_out, "dq_out", shape, dtype, dev)
+    _launch("attn_rope_bwd", lib.attn_rope_bwd, dev, stream, *_rows(dq, "dq", shape), *kr, *xq, *xk, dq_out.data_ptr(), k_to,
+            wq_to, wk_to, fp, rotary, bool(interleaved), factor, pp, ps, wq, wk, eps, ws, code, B, Hq, Hkv, L, d)
+    if wq is None:
+        return dq_out, dk_out
+    return dq_out, dk_out, dq_weight, (dk_weight if dk is not None else None)
 
 
 def attn_rope_bwd_workspace_bytes(d: int) -> int:
@@ -551,36 +586,22 @@ def attn_rope_bwd_workspace_bytes(d: int) -> int:
     return int(n)
 
 
-def _workspace(workspace, nbytes, like, stream):
-    if workspace is None:
-        return _empty((nbytes // 4,), torch.float32, like.device, stream)
-    if (workspace.device != like.device or not workspace.is_contiguous()
-            or workspace.numel() * workspace.element_size() < nbytes):
-        raise ValueError(f"gbattn: workspace must be a contiguous CUDA tensor of at least {nbytes} bytes on the device "
-                         "of the other tensors")
-    return workspace
-
-
-def _cache(k_pages, v_pages, like=None):
-    """(k pointer, v pointer, page, head and slot strides, pages, slots of a page), and the shape."""
-    code = _dtype_code(k_pages, "k_pages")
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+def _cache(k_pages, v_pages):
+    """Device index, type code, shape, and (k pointer, v pointer, page, head and slot strides, pages, slots of a page)."""
+    dev, code = _device_and_type(k_pages, "k_pages")
+    shape = k_pages.shape
+    if len(shape) != 4 or v_pages.shape != shape:
         raise ValueError("gbattn: k_pages and v_pages must share one [pages, Hkv, page, d] shape")
-    if v_pages.dtype != k_pages.dtype or v_pages.device != k_pages.device:
+    if v_pages.dtype != k_pages.dtype or v_pages.get_device() != dev:
         raise ValueError("gbattn: k_pages and v_pages must share their type and device")
-    if like is not None:
-        _check_like(like, "q, k and v", k_pages)
-    P, H, page, d = k_pages.shape
-    sp, sh, ss, sd = k_pages.stride()
-    vp, vh, vs, vd = v_pages.stride()
-    if sd != 1 or vd != 1:
+    P, H, page, _ = shape
+    strides, v_strides = k_pages.stride(), v_pages.stride()
+    sp, sh, ss, sd = strides
+    if sd != 1 or v_strides[3] != 1:
         raise ValueError("gbattn: the last dimension of k_pages and v_pages must be contiguous")
-    if (P > 1 and sp != vp) or (H > 1 and sh != vh) or (page > 1 and ss != vs):
+    if v_strides != strides and any(n > 1 and a != b for n, a, b in zip(shape, strides, v_strides)):
         raise ValueError("gbattn: k_pages and v_pages must share their strides")
-    sh = sh if H > 1 else 0
-    if P <= 1:
-        sp = 0
-    return code, (k_pages.data_ptr(), v_pages.data_ptr(), sp, sh, ss, P, page), (H, d)
+    return dev, code, shape, (k_pages.data_ptr(), v_pages.data_ptr(), sp if P > 1 else 0, sh if H > 1 else 0, ss, P, page)
 
 
 def attn_cache_append(k, v, k_pages, v_pages, table, lengths, counts=None, q=None, inv_freq=None,
@@ -593,30 +614,30 @@ def attn_cache_append(k, v, k_pages, v_pages, table, lengths, counts=None, q=Non
     all), at positions lengths - counts ...  With inv_freq (and q_weight, k_weight) the keys
     are rotated (and normalised) on the way as by attn_rope, and so is q [B, Hq, L, d], whose
     result is returned (q_out; zeros in rows behind counts).  Enqueued on `stream`."""
-    code, cache, (Hkv, d) = _cache(k_pages, v_pages, k)
-    if k.dim() != 4 or k.shape[1] != Hkv or k.shape[3] != d:
-        raise ValueError("gbattn: k must be [B, Hkv, L, d] with the cache's Hkv and d")
-    _check_like(v, "v", k, k.shape)
-    B, _, L, _ = k.shape
-    Hq = 0
-    qr = _NO_ROWS
+    dev, code, (_, Hkv, _, d), cache = _cache(k_pages, v_pages)
+    dtype, shape = k_pages.dtype, k.shape
+    if len(shape) != 4 or shape[1] != Hkv or shape[3] != d or v.shape != shape:
+        raise ValueError("gbattn: k and v must be [B, Hkv, L, d] with the cache's Hkv and d")
+    _check_like(k, "k", dev, dtype)
+    _check_like(v, "v", dev, dtype)
+    B, _, L, _ = shape
+    Hq, qr, q_to = 0, _NO_ROWS, None
     if q is not None:
-        if q.dim() != 4 or q.shape[0] != B or q.shape[2] != L or q.shape[3] != d:
+        q_shape = q.shape
+        if len(q_shape) != 4 or q_shape[0] != B or q_shape[2] != L or q_shape[3] != d:
             raise ValueError("gbattn: q must be [B, Hq, L, d] like k")
-        _check_like(q, "q", k)
-        Hq = q.shape[1]
-        qr = _rows(q, "q")
-        q_out = _out(q_out, "q_out", q.shape, q.dtype, q, stream)
-    if table.dim() != 2:
-        raise ValueError("gbattn: table must be [B, width]")
-    tp, ts = _ints(table, "table", (B, table.shape[1]), k)
-    lp, _ = _ints(lengths, "lengths", (B,), k)
-    cp = _ints(counts, "counts", (B,), k)[0] if counts is not None else None
-    fp, rotary = _frequencies(inv_freq, d, k)
-    wq, wk = _norm_weights(q_weight, k_weight, d, k, q is not None, True)
-    _launch("attn_cache_append", load_library().attn_cache_append, k.device, stream, *_rows(k, "k"), *_rows(v, "v"), *qr,
-            q_out.data_ptr() if q is not None else None, *cache, tp, ts, table.shape[1], lp, cp, fp, rotary,
-            int(bool(interleaved)), float(factor), wq, wk, float(eps), code, B, Hq, Hkv, L, d)
+        _check_like(q, "q", dev, dtype)
+        Hq, qr = q_shape[1], _rows(q, "q", q_shape)
+        q_out = _empty(q_shape, dtype, q, stream) if q_out is None else _check_out(q_out, "q_out", q_shape, dtype, dev)
+        q_to = q_out.data_ptr()
+    tp, ts, tw = _int_rows(table, "table", B, dev)
+    lp = _ints(lengths, "lengths", B, dev)
+    cp = _ints(counts, "counts", B, dev) if counts is not None else None
+    fp, rotary = _frequencies(inv_freq, dev)
+    wq, wk = _norm_weights(q_weight, k_weight, d, dev, dtype, q is not None, True)
+    _launch("attn_cache_append", (_lib or load_library()).attn_cache_append, dev, stream, *_rows(k, "k", shape),
+            *_rows(v, "v", shape), *qr, q_to, *cache, tp, ts, tw, lp, cp, fp, rotary, bool(interleaved), factor, wq, wk, eps,
+            code, B, Hq, Hkv, L, d)
     return q_out if q is not None else None
 
 
@@ -632,11 +653,11 @@ def attn_cache_copy(k_pages, v_pages, src, dst, stream=None) -> None:
     """Copy pages of a cache, keys and values: page src[i] to page dst[i], one after the other (also
     where a page occurs more than once).  src and dst are page numbers on the host (lists or
     int32 CPU tensors), read before the call returns.  Enqueued on `stream`."""
-    _, cache, (Hkv, d) = _cache(k_pages, v_pages)
+    dev, _, (_, Hkv, _, d), cache = _cache(k_pages, v_pages)
     src, dst = _page_list(src, "src"), _page_list(dst, "dst")
     if src.shape != dst.shape:
         raise ValueError("gbattn: src and dst must have the same length")
-    _launch("attn_cache_copy", load_library().attn_cache_copy, k_pages.device, stream, *cache, Hkv, d, src.data_ptr(),
+    _launch("attn_cache_copy", (_lib or load_library()).attn_cache_copy, dev, stream, *cache, Hkv, d, src.data_ptr(),
             dst.data_ptr(), src.shape[0])
 
 
@@ -656,28 +677,24 @@ def attn_decode_paged(q, k_pages, v_pages, table, lengths, scale: float | None =
     sequence gives zeros and -inf.  Outputs, and the workspace unless given (a contiguous CUDA
     tensor of attn_decode_paged_workspace_bytes bytes), are allocated by torch.  Enqueued on
     `stream`."""
-    code, cache, (Hkv, d) = _cache(k_pages, v_pages, q)
-    if q.dim() == 4 and q.shape[2] == 1:
-        q = q[:, :, 0]
-    if q.dim() != 3 or q.shape[2] != d:
+    dev, code, (_, Hkv, _, d), cache = _cache(k_pages, v_pages)
+    shape, strides = q.shape, q.stride()
+    if len(shape) not in (3, 4) or shape[-1] != d or (len(shape) == 4 and shape[2] != 1):
         raise ValueError("gbattn: q must be [B, Hq, d] or [B, Hq, 1, d] with the cache's d")
-    B, Hq, _ = q.shape
-    if q.stride(2) != 1:
+    _check_like(q, "q", dev, k_pages.dtype)
+    B, Hq = shape[0], shape[1]
+    if strides[-1] != 1:
         raise ValueError("gbattn: the last dimension of q must be contiguous")
-    if table.dim() != 2:
-        raise ValueError("gbattn: table must be [B, width]")
-    tp, ts = _ints(table, "table", (B, table.shape[1]), q)
-    lp, _ = _ints(lengths, "lengths", (B,), q)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    o = _out(o, "o", (B, Hq, d), q.dtype, q, stream)
-    lse = _out(lse, "lse", (B, Hq), torch.float32, q, stream)
-    lib = load_library()
+    tp, ts, tw = _int_rows(table, "table", B, dev)
+    lp = _ints(lengths, "lengths", B, dev)
+    o = _empty((B, Hq, d), q.dtype, q, stream) if o is None else _check_out(o, "o", (B, Hq, d), q.dtype, dev)
+    lse = _empty((B, Hq), torch.float32, q, stream) if lse is None else _check_out(lse, "lse", (B, Hq), torch.float32, dev)
+    lib = _lib or load_library()
     nbytes = lib.attn_decode_paged_workspace_bytes(Hq, Hkv, d)
     if nbytes < 0:
         raise GbattnError(int(nbytes), "attn_decode_paged_workspace_bytes")
-    workspace = _workspace(workspace, nbytes, q, stream)
-    _launch("attn_decode_paged", lib.attn_decode_paged, q.device, stream, q.data_ptr(), q.stride(0) if B > 1 else 0,
-            q.stride(1) if Hq > 1 else 0, *cache, tp, ts, table.shape[1], lp, o.data_ptr(), lse.data_ptr(),
-            workspace.data_ptr(), code, B, Hq, Hkv, d, float(scale))
+    workspace = _workspace(workspace, nbytes, q, dev, stream)
+    _launch("attn_decode_paged", lib.attn_decode_paged, dev, stream, q.data_ptr(), strides[0] if B > 1 else 0,
+            strides[1] if Hq > 1 else 0, *cache, tp, ts, tw, lp, o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), code, B, Hq,
+            Hkv, d, 1.0 / math.sqrt(d) if scale is None else scale)
     return o, lse
