@@ -30,7 +30,7 @@ struct Span {  // bytes [p, p + n)
 bool finite_nonneg(float x) { return std::isfinite(x) && x >= 0.f; }
 bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256 || d == 512; }
 bool stride_ok(long long s) { return s >= 0 && s % 8 == 0 && s < (1LL << 39); }
-bool rows_ok(const Rows &r) { return stride_ok(r.sb) && stride_ok(r.sh) && stride_ok(r.sl); }
+bool rows_ok(const Rows &r) { return stride_ok(r.sb) && stride_ok(r.sh) && r.sh < (1LL << 32) && stride_ok(r.sl); }
 
 Span rows_span(const Rows &r, int B, int H, int L, int d) {
   if (!r.p) return {nullptr, 0};
@@ -58,7 +58,8 @@ int check_dims(int dtype, int B, int Hq, int Hkv, int L, int d) {
   if (heads > INT_MAX / 4 || static_cast<long long>(B) * L > INT_MAX / 4 ||
       heads > (1LL << 40) / (static_cast<long long>(B) * L))
     return GBATTN_ERR_DIMS;
-  return head_dim_ok(d) ? GBATTN_OK : GBATTN_ERR_HEAD_DIM;
+  if (!head_dim_ok(d)) return GBATTN_ERR_HEAD_DIM;
+  return static_cast<long long>(L) * d < (1LL << 32) ? GBATTN_OK : GBATTN_ERR_DIMS;
 }
 
 int check_rope(const double *inv_freq, int rotary, float factor, float eps, const int *positions, long long positions_stride,
@@ -93,7 +94,7 @@ int check_pages(const void *k, const void *v, long long sp, long long sh, long l
                 long long *extent) {
   if (pages <= 0 || Hkv <= 0) return GBATTN_ERR_DIMS;
   if (page <= 0 || page % 8) return GBATTN_ERR_PAGES;
-  if (!stride_ok(sp) || !stride_ok(sh) || !stride_ok(ss)) return GBATTN_ERR_STRIDE;
+  if (!stride_ok(sp) || !stride_ok(sh) || sh >= (1LL << 32) || !stride_ok(ss)) return GBATTN_ERR_STRIDE;
   const long long slots = (page - 1LL) * ss + d, heads = (Hkv - 1LL) * sh + d;
   const bool head_outer = ss >= d && (Hkv == 1 || sh >= slots), slot_outer = (Hkv == 1 || sh >= d) && ss >= heads;
   if (!head_outer && !slot_outer) return GBATTN_ERR_STRIDE;

@@ -1,16 +1,21 @@
 // rope.cu -- rotary positions, per-head norms and the paged append: kernels and launches.
 //
 // Every kernel is one pass over its rows and bound by their reads and writes.  A row of d
-// elements belongs to d / 16 consecutive lanes (4, 8, 16, 32 for d = 64, 128, 256, 512); a
-// lane holds two 16-byte vectors that contain both halves of every pair it turns, so that
-// neither layout needs an exchange between lanes:
-//     half layout, lane j < rotary / 16:  elements 8j .. 8j+7 and rotary/2 + 8j .. +7
-//     otherwise (interleaved, and the elements behind `rotary`):  16j .. 16j+15
-// and in both layouts lane j turns its pairs by the angles 8j .. 8j+7.  The norm's sum of
-// squares is a shuffle reduction over the row's lanes.
-// A block takes `tokens` consecutive (batch, row) positions; their cosines and sines are
-// computed once, into shared memory, and each thread keeps the eight that it needs in
-// registers while it walks over the heads of its token.
+// elements belongs to consecutive lanes of one warp, E elements each: 8 (8, 16, 32 lanes for
+// d = 64, 128, 256), or 16 at d = 512.  A lane holds two vectors of E / 2 elements that contain both
+// halves of every pair it turns, so that neither layout needs an exchange between lanes:
+//     half layout, lane j < rotary / E:  elements E/2 j .. and rotary/2 + E/2 j ..
+//     otherwise (interleaved, and the elements behind `rotary`):  E j .. E j + E - 1
+// and in both layouts lane j turns its pairs by the angles E/2 j .. E/2 j + E/2 - 1.  The norm's
+// sum of squares is a shuffle reduction over the row's lanes.
+//
+// The work is cut into units, `at_once` rows for each thread: a tile of `tokens` consecutive
+// (batch, row) positions times a run of heads of the joint list (q, k and, for the append, v).
+// As many blocks as fit the GPU at once take equal runs of consecutive units, so that none is
+// left with a thin last wave (1024 blocks of a tile each, three to an SM, took 44.7 us for
+// norm and rotation of 4 x 40 x 2048 x 128 in bf16).  A unit's loads are all issued before its
+// first row is worked on; a new tile's cosines and sines are computed once, into shared
+// memory, behind them, and each thread keeps those of its token in registers.
 //
 // Angles: position x inv_freq is reduced in integers.  inv_freq / 2 pi becomes a 64-bit
 // binary fraction of a turn; its product with the position, taken modulo 2^64, is the angle
@@ -22,8 +27,38 @@
 #include "rope.cuh"
 #include "vec16.cuh"
 
+#ifndef AO
+#define AO 4
+#endif
+#ifndef LB
+#define LB 3
+#endif
+#ifndef LBN
+#define LBN 3
+#endif
+#ifndef BU
+#define BU 2
+#endif
+#ifndef LBB
+#define LBB 3
+#endif
+#ifndef RT
+#define RT 32
+#endif
+#ifndef RB
+#define RB 4
+#endif
+
 namespace gbattn {
 namespace {
+
+// Rows that a thread loads before it works on the first.
+template <int E>
+constexpr int kAtOnce = E == 8 ? AO : 2;
+template <int E>
+constexpr int kBwdAtOnce = E == 8 ? BU : 1;
+// Blocks that share an SM (the kernels' launch bounds).
+constexpr int rope_resident(int E, bool norm) { return E == 16 ? 2 : norm ? LBN : LB; }
 
 // frac(x / 2 pi) 2^64 of a finite double x = m 2^e (m an integer of at most 53 bits):
 // m C 2^(e - 2) with C = 2^66 / 2 pi, as a 128-bit integer, modulo 2^64.
@@ -47,13 +82,13 @@ __device__ __forceinline__ uint64_t turns_fixed(double x) {
   return (bits >> 63) ? 0ull - f : f;
 }
 
-// factor * (cos, sin) of position * freq
-__device__ __forceinline__ float2 turn_of(int position, double freq, float factor, float sign) {
-  const int64_t turn = static_cast<int64_t>(static_cast<uint64_t>(static_cast<int64_t>(position)) * turns_fixed(freq));
+// factor * (cos, sin) of position * freq, freq as turns_fixed gave it.  The upper 32 bits of the
+// angle are enough: an error of 2^-32 turns is far below the fp32 sine's own.
+__device__ __forceinline__ float2 turn_of(int position, uint64_t freq, float factor, float sign) {
+  const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(position)) * freq;
   float s, c;
-  sincospif(static_cast<float>(turn) * 0x1p-63f, &s, &c);
-  const bool bad = (static_cast<uint64_t>(__double_as_longlong(freq)) & 0x7ff0000000000000ull) == 0x7ff0000000000000ull;
-  return bad ? make_float2(NAN, NAN) : make_float2(factor * c, sign * factor * s);
+  sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f, &s, &c);
+  return make_float2(factor * c, sign * factor * s);
 }
 
 struct Place {       // where a thread works
@@ -62,334 +97,515 @@ struct Place {       // where a thread works
   int lane;          // lane j within the row
 };
 
-template <bool INTER>
+template <bool INTER, int E>
 __device__ __forceinline__ Place place_of(const RopeParams &p, int lpr) {
   Place r;
   r.lane = threadIdx.x & (lpr - 1);
-  r.turns = r.lane < (p.rotary >> 4);
+  r.turns = r.lane < p.rotary / E;
   const bool split = !INTER && r.turns;
-  r.c0 = split ? 8 * r.lane : 16 * r.lane;
-  r.c1 = split ? 8 * r.lane + (p.rotary >> 1) : 16 * r.lane + 8;
+  r.c0 = split ? E / 2 * r.lane : E * r.lane;
+  r.c1 = split ? E / 2 * r.lane + (p.rotary >> 1) : E * r.lane + E / 2;
   return r;
 }
 
-__device__ __forceinline__ float row_sum(float x, int lpr) {
-  for (int o = 1; o < lpr; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
+// E / 2 16-bit values as they lie in memory.
+template <int E>
+struct Vec {
+  uint32_t w[E / 4];
+};
+template <int E>
+__device__ __forceinline__ Vec<E> load_vec(const uint16_t *p) {
+  Vec<E> v;
+  if constexpr (E == 8) {
+    const uint2 t = __ldg(reinterpret_cast<const uint2 *>(p));
+    v.w[0] = t.x;
+    v.w[1] = t.y;
+  } else {
+    const uint4 t = __ldg(reinterpret_cast<const uint4 *>(p));
+    v.w[0] = t.x;
+    v.w[1] = t.y;
+    v.w[2] = t.z;
+    v.w[3] = t.w;
+  }
+  return v;
+}
+template <int E>
+__device__ __forceinline__ void store_vec(uint16_t *p, const Vec<E> &v) {
+  if constexpr (E == 8)
+    *reinterpret_cast<uint2 *>(p) = make_uint2(v.w[0], v.w[1]);
+  else
+    *reinterpret_cast<uint4 *>(p) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+}
+template <int E>
+__device__ __forceinline__ Vec<E> zero_vec() {
+  Vec<E> v;
+#pragma unroll
+  for (int i = 0; i < E / 4; ++i) v.w[i] = 0u;
+  return v;
+}
+// A lane's elements as fp32 pairs: A the first elements of its rotary pairs, B the second, two
+// rotary pairs to an fp32x2 register, so that all arithmetic runs two elements an instruction.
+// Half layout: word i of the first vector is A[i], of the second B[i].  Interleaved: words 2i
+// and 2i + 1 (of the lane's E / 2) hold A[i], B[i] as their low and high halves.
+template <int E>
+struct Pairs {
+  uint64_t A[E / 4], B[E / 4];
+};
+template <bool BF, bool INTER, int E>
+__device__ __forceinline__ void unpack(const Vec<E> &a, const Vec<E> &b, Pairs<E> &x) {
+#pragma unroll
+  for (int i = 0; i < E / 4; ++i) {
+    const uint32_t u = INTER ? (2 * i < E / 4 ? a.w[2 * i] : b.w[2 * i - E / 4]) : a.w[i];
+    const uint32_t v = INTER ? (2 * i < E / 4 ? a.w[2 * i + 1] : b.w[2 * i + 1 - E / 4]) : b.w[i];
+    float u0, u1, v0, v1;
+    unpack2<BF>(u, u0, u1);
+    unpack2<BF>(v, v0, v1);
+    x.A[i] = INTER ? f32x2(u0, v0) : f32x2(u0, u1);
+    x.B[i] = INTER ? f32x2(u1, v1) : f32x2(v0, v1);
+  }
+}
+template <bool BF, bool INTER, int E>
+__device__ __forceinline__ void store_row(uint16_t *row, const Place &at, const Pairs<E> &x) {
+  Vec<E> a, b;
+#pragma unroll
+  for (int i = 0; i < E / 4; ++i) {
+    float p0, p1, q0, q1;
+    f32x2_split(x.A[i], p0, p1);
+    f32x2_split(x.B[i], q0, q1);
+    const uint32_t u = INTER ? pack2<BF>(p0, q0) : pack2<BF>(p0, p1), v = INTER ? pack2<BF>(p1, q1) : pack2<BF>(q0, q1);
+    if constexpr (INTER) {
+      (2 * i < E / 4 ? a.w[2 * i] : b.w[2 * i - E / 4]) = u;
+      (2 * i < E / 4 ? a.w[2 * i + 1] : b.w[2 * i + 1 - E / 4]) = v;
+    } else {
+      a.w[i] = u;
+      b.w[i] = v;
+    }
+  }
+  store_vec<E>(row + at.c0, a);
+  store_vec<E>(row + at.c1, b);
 }
 
-// Turn the pairs of (x0, x1) in place; e-th pair by (c[e], s[e]).
-template <bool INTER>
-__device__ __forceinline__ void turn_pairs(float *x, const float *c, const float *s) {
+// Cosines, sines and negated sines of a lane's pairs (1, 0 where it does not turn).
+template <int E>
+struct Turn {
+  uint64_t c[E / 4], s[E / 4], n[E / 4];
+};
+template <int E>
+__device__ __forceinline__ void turn_pairs(Pairs<E> &x, const Turn<E> &t) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int i = INTER ? 2 * e : e, j = INTER ? 2 * e + 1 : e + 8;
-    const float a = x[i], b = x[j];
-    x[i] = a * c[e] - b * s[e];
-    x[j] = b * c[e] + a * s[e];
+  for (int i = 0; i < E / 4; ++i) {
+    const uint64_t a = x.A[i], b = x.B[i];
+    x.A[i] = ffma2(b, t.n[i], fmul2(a, t.c[i]));
+    x.B[i] = ffma2(a, t.s[i], fmul2(b, t.c[i]));
   }
 }
 
-__device__ __forceinline__ uint4 load16(const uint16_t *p) { return __ldg(reinterpret_cast<const uint4 *>(p)); }
-__device__ __forceinline__ void store16(uint16_t *p, uint4 v) { *reinterpret_cast<uint4 *>(p) = v; }
-
-constexpr int kHeadsAtOnce = 4;  // rows a thread loads before it works on the first
-
-// Rows of heads [h0, h1) of one tensor at one token: norm, turn, store.  Every thread of the
-// block runs the same number of steps (the shuffles need whole rows).
-template <bool BF, bool NORM, bool INTER>
-__device__ __forceinline__ void rope_heads(const uint16_t *src, long long src_h, uint16_t *dst, long long dst_h, int h0,
-                                           int h1, int group, int groups, bool valid, const Place &at, int lpr,
-                                           const float *c, const float *s, const uint16_t *weight, float eps, float inv_d) {
-  if (h0 >= h1) return;
-  float w[16];
-  if constexpr (NORM) {
-    vec_unpack<BF>(load16(weight + at.c0), w);
-    vec_unpack<BF>(load16(weight + at.c1), w + 8);
+// The norms' weights as fp32 in shared memory, q's, then k's, each in the order in which a lane's
+// pairs want them: lane j's A and B at E j and E j + E / 2.
+template <bool BF, bool INTER, int E>
+__device__ __forceinline__ void fill_weights(float *weights, const RopeParams &p) {
+  for (int i = threadIdx.x; i < 2 * p.d; i += kRopeThreads) {
+    const bool is_q = i < p.d;
+    const uint16_t *const w = static_cast<const uint16_t *>(is_q ? p.q_w : p.k_w);
+    if (!w) continue;
+    const int k = is_q ? i : i - p.d, j = k / E, e = k % E, half = e / (E / 2), r = e % (E / 2);  // lane, A or B, place there
+    const bool split = !INTER && j < p.rotary / E;
+    // unpack's order: interleaved pairs where INTER; else the lane's first and second vector
+    const int from = split ? half * (p.rotary >> 1) + E / 2 * j + r : INTER ? E * j + 2 * r + half : E * j + half * (E / 2) + r;
+    float lo, hi;
+    unpack2<BF>(w[from], lo, hi);
+    weights[i] = lo;
   }
-  for (int base = h0; base < h1; base += groups * kHeadsAtOnce) {
-    uint4 a[kHeadsAtOnce], b[kHeadsAtOnce];
+}
+template <int E>
+__device__ __forceinline__ void weight_pairs(const float *w, int lane, Pairs<E> &out) {
 #pragma unroll
-    for (int u = 0; u < kHeadsAtOnce; ++u) {
-      const int h = base + u * groups + group;
-      a[u] = b[u] = make_uint4(0, 0, 0, 0);
-      if (valid && h < h1) {
-        a[u] = load16(src + h * src_h + at.c0);
-        b[u] = load16(src + h * src_h + at.c1);
+  for (int i = 0; i < E / 4; i += 2) {
+    const float4 a = *reinterpret_cast<const float4 *>(w + E * lane + 2 * i);
+    const float4 b = *reinterpret_cast<const float4 *>(w + E * lane + E / 2 + 2 * i);
+    out.A[i] = f32x2(a.x, a.y);
+    out.A[i + 1] = f32x2(a.z, a.w);
+    out.B[i] = f32x2(b.x, b.y);
+    out.B[i + 1] = f32x2(b.z, b.w);
+  }
+}
+
+// sum of x y over a row's lanes
+template <int E>
+__device__ __forceinline__ float lane_dot(const Pairs<E> &x, const Pairs<E> &y) {
+  uint64_t t = fmul2(x.A[0], y.A[0]);
+  t = ffma2(x.B[0], y.B[0], t);
+#pragma unroll
+  for (int i = 1; i < E / 4; ++i) {
+    t = ffma2(x.A[i], y.A[i], t);
+    t = ffma2(x.B[i], y.B[i], t);
+  }
+  float lo, hi;
+  f32x2_split(t, lo, hi);
+  return lo + hi;
+}
+
+// The block's frequencies as fixed-point turns, and the factor of each pair (NaN where the
+// frequency is not finite).
+struct Frequencies {
+  uint64_t turns[256];
+  float factor[256];
+};
+__device__ __forceinline__ void fill_frequencies(Frequencies &f, const RopeParams &p) {
+  for (int i = threadIdx.x; i < (p.rotary >> 1); i += kRopeThreads) {
+    const double x = p.inv_freq[i];
+    f.turns[i] = turns_fixed(x);
+    f.factor[i] = isfinite(x) ? p.factor : NAN;
+  }
+}
+// The tile's cosines and sines: entry [r][token], r a pair's number.
+__device__ __forceinline__ void fill_turns(float2 *table, const int *pos, const Frequencies &f, const RopeParams &p) {
+  const int shift = 31 - __clz(p.tokens);
+  for (int i = threadIdx.x; i < (p.rotary >> 1) << shift; i += kRopeThreads) {
+    const int r = i >> shift;
+    table[i] = turn_of(pos[i & (p.tokens - 1)], f.turns[r], f.factor[r], p.sign);
+  }
+}
+template <int E>
+__device__ __forceinline__ void load_turns(const float2 *table, int token, int tokens, const Place &at, Turn<E> &t) {
+#pragma unroll
+  for (int i = 0; i < E / 4; ++i) {
+    float2 x = make_float2(1.f, 0.f), y = x;
+    if (at.turns) {
+      x = table[(E / 2 * at.lane + 2 * i) * tokens + token];
+      y = table[(E / 2 * at.lane + 2 * i + 1) * tokens + token];
+    }
+    t.c[i] = f32x2(x.x, y.x);
+    t.s[i] = f32x2(x.y, y.y);
+    t.n[i] = f32x2(-x.y, -y.y);
+  }
+}
+
+// The units of this block, as a run over tiles and steps; a step is a run of heads of one tensor.
+struct Units {
+  long long tile;
+  int step;
+  long long left;
+};
+__device__ __forceinline__ Units units_of(const RopeParams &p) {
+  const long long u0 = p.units * blockIdx.x / gridDim.x, u1 = p.units * (blockIdx.x + 1) / gridDim.x;
+  Units u;
+  u.tile = u0 / p.steps;
+  u.step = static_cast<int>(u0 - u.tile * p.steps);
+  u.left = u1 - u0;
+  return u;
+}
+
+// A thread's token in the current tile.
+struct Token {
+  long long b, l;
+  bool in;  // whether there is one
+};
+__device__ __forceinline__ Token token_of(const RopeParams &p, long long n) {
+  Token t;
+  t.in = n < static_cast<long long>(p.B) * p.L;
+  const uint32_t b = t.in ? static_cast<uint32_t>(n) / static_cast<uint32_t>(p.L) : 0;  // B L fits 31 bits
+  t.b = b;
+  t.l = t.in ? n - static_cast<long long>(b) * p.L : 0;
+  return t;
+}
+__device__ __forceinline__ const uint16_t *row_at(const void *p, const Token &t, const long long *strides) {
+  return static_cast<const uint16_t *>(p) + t.b * strides[0] + t.l * strides[2];
+}
+
+// attn_rope and (APPEND) attn_cache_append.  The append's new tokens of sequence b are counts[b]
+// rows (all L without counts) at positions lengths[b] - counts[b] .. lengths[b] - 1; their keys
+// and values go to the pages that the table names, their queries to q_out (zeros behind the
+// last token).
+template <bool BF, bool NORM, bool INTER, int E, bool APPEND>
+__global__ void __launch_bounds__(kRopeThreads, E == 16 ? 2 : NORM ? LBN : LB) rope_kernel(const RopeParams p) {
+  constexpr int U = kAtOnce<E>;
+  extern __shared__ float2 turns[];
+  __shared__ int pos[kRopeMaxTokens];
+  __shared__ long long cell[APPEND ? kRopeMaxTokens : 1];  // element offset of the page slot, -1: none, -2: behind the last token
+  __shared__ Frequencies freq;
+  __shared__ __align__(16) float weights[NORM ? 1024 : 4];
+  grid_launch_dependents();
+  grid_wait_prior();
+  const int lpr = p.d / E, groups = kRopeThreads / lpr / p.tokens;
+  const Place at = place_of<INTER, E>(p, lpr);
+  const int row = threadIdx.x / lpr, token = row / groups, group = row - token * groups;
+  const uint32_t out_h = static_cast<uint32_t>(p.L) * static_cast<uint32_t>(p.d);  // below 2^32
+  const bool plain = APPEND && !NORM && p.rotary == 0;
+  const float inv_d = 1.f / static_cast<float>(p.d);  // exact: a power of two
+  if constexpr (NORM) fill_weights<BF, INTER, E>(weights, p);
+  fill_frequencies(freq, p);
+  Units u = units_of(p);
+  bool fresh = true;
+  Token tok;
+  long long to = 0;
+  Turn<E> turn;
+  for (; u.left > 0; --u.left) {
+    const long long n0 = u.tile * p.tokens;
+    if (fresh) tok = token_of(p, n0 + token);
+    // The unit's tensor, heads and source; the same in every thread but for the token.
+    const int kind = u.step < p.steps_q ? 0 : u.step < p.steps_q + p.steps_k ? 1 : 2;
+    const int heads = kind == 0 ? p.Hq : p.Hkv;
+    const int h0 = (u.step - (kind == 0 ? 0 : kind == 1 ? p.steps_q : p.steps_q + p.steps_k)) * groups * p.at_once + group;
+    const long long *const strides = kind == 0 ? p.qs : kind == 1 ? p.ks : p.vs;
+    const uint32_t src_h = static_cast<uint32_t>(strides[1]);
+    const uint16_t *src = row_at(kind == 0 ? p.q : kind == 1 ? p.k : p.v, tok, strides) + static_cast<uint64_t>(h0) * src_h;
+    const int rows_here = tok.in && h0 < heads ? min(p.at_once, (heads - h0 + groups - 1) / groups) : 0;  // of this thread
+    Vec<E> a[U], b[U];
+    {
+      const uint64_t step = static_cast<uint64_t>(groups) * src_h;
+      const uint16_t *from = src;
+#pragma unroll
+      for (int i = 0; i < U; ++i, from += step) {
+        a[i] = b[i] = zero_vec<E>();
+        if (i < rows_here) {
+          a[i] = load_vec<E>(from + at.c0);
+          b[i] = load_vec<E>(from + at.c1);
+        }
       }
     }
+    if (fresh) {  // the same in every thread
+      fresh = false;
+      __syncthreads();  // the tile before is done with the tables
+      if (threadIdx.x < p.tokens) {
+        const Token t = token_of(p, n0 + threadIdx.x);
+        int x = 0;
+        if constexpr (!APPEND) {
+          if (t.in) x = p.positions ? p.positions[t.b * p.pos_s + t.l] : static_cast<int>(t.l);
+        } else {
+          long long cl = -2;
+          if (t.in) {
+            const int len = p.lengths[t.b], count = p.counts ? p.counts[t.b] : p.L;
+            if (count < 0 || count > p.L || len < count || len > static_cast<long long>(p.table_w) * p.page) {
+              atomicCAS(p.status, 0u, kDevBadLength);
+            } else if (t.l < count) {
+              x = len - count + static_cast<int>(t.l);
+              const int index = x / p.page, page = p.table[t.b * p.table_s + index];
+              cl = -1;
+              if (page < 0 || page >= p.pages)
+                atomicCAS(p.status, 0u, kDevBadPage);
+              else
+                cl = page * p.page_s + static_cast<long long>(x - index * p.page) * p.slot_s;
+            }
+          }
+          cell[threadIdx.x] = cl;
+        }
+        pos[threadIdx.x] = x;
+      }
+      __syncthreads();
+      if (p.rotary > 0) {
+        fill_turns(turns, pos, freq, p);
+        __syncthreads();
+      }
+      load_turns<E>(turns, token, p.tokens, at, turn);
+      if constexpr (APPEND) to = cell[token];
+    }
+    const bool paged = APPEND && kind != 0;
+    const uint32_t dst_h = paged ? static_cast<uint32_t>(p.head_s) : out_h;
+    uint16_t *dst = static_cast<uint16_t *>(paged ? (kind == 1 ? p.k_pages : p.v_pages) : kind == 0 ? p.q_out : p.k_out) +
+                    (paged ? max(to, 0LL) : tok.b * heads * static_cast<long long>(out_h) + tok.l * p.d) + static_cast<uint64_t>(h0) * dst_h;
+    const bool copies = APPEND && (plain || kind == 2), clears = APPEND && kind == 0 && to == -2;
+    const int stored = APPEND && kind != 0 && to < 0 ? 0 : rows_here;
+    const uint64_t step = static_cast<uint64_t>(groups) * dst_h;
+    if (copies || clears) {
 #pragma unroll
-    for (int u = 0; u < kHeadsAtOnce; ++u) {
-      const int h = base + u * groups + group;
-      float x[16];
-      vec_unpack<BF>(a[u], x);
-      vec_unpack<BF>(b[u], x + 8);
+      for (int i = 0; i < U; ++i)
+        if (i < stored) {
+          store_vec<E>(dst + i * step + at.c0, clears ? zero_vec<E>() : a[i]);
+          store_vec<E>(dst + i * step + at.c1, clears ? zero_vec<E>() : b[i]);
+        }
+    }
+    if (!copies) {  // the same in every thread: the shuffles need whole rows
+      Pairs<E> x[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) unpack<BF, INTER, E>(a[i], b[i], x[i]);
       if constexpr (NORM) {
-        float ss = 0.f;
+        Pairs<E> w;
+        weight_pairs<E>(weights + (kind == 0 ? 0 : p.d), at.lane, w);
+        float ss[U];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
-        const float rstd = rsqrtf(row_sum(ss, lpr) * inv_d + eps);
+        for (int i = 0; i < U; ++i) ss[i] = lane_dot<E>(x[i], x[i]);
+        for (int o = 1; o < lpr; o <<= 1)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = x[e] * rstd * w[e];
+          for (int i = 0; i < U; ++i) ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], o);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const float rstd = rsqrtf(ss[i] * inv_d + p.eps);
+          const uint64_t r = f32x2(rstd, rstd);
+#pragma unroll
+          for (int e = 0; e < E / 4; ++e) {
+            x[i].A[e] = fmul2(fmul2(x[i].A[e], r), w.A[e]);
+            x[i].B[e] = fmul2(fmul2(x[i].B[e], r), w.B[e]);
+          }
+        }
       }
-      if (at.turns) turn_pairs<INTER>(x, c, s);
-      if (valid && h < h1) {
-        store16(dst + h * dst_h + at.c0, vec_pack<BF>(x));
-        store16(dst + h * dst_h + at.c1, vec_pack<BF>(x + 8));
-      }
+      if (at.turns)
+#pragma unroll
+        for (int i = 0; i < U; ++i) turn_pairs<E>(x[i], turn);
+      const int out = clears ? 0 : stored;
+#pragma unroll
+      for (int i = 0; i < U; ++i, dst += step)
+        if (i < out) store_row<BF, INTER, E>(dst, at, x[i]);
+    }
+    if (++u.step == p.steps) {
+      u.step = 0;
+      ++u.tile;
+      fresh = true;
     }
   }
 }
 
-// Fill the block's table of cosines and sines: entry [token][r].
-__device__ __forceinline__ void fill_turns(float2 *table, const int *pos, const RopeParams &p) {
-  const int half = p.rotary >> 1;
-  for (int i = threadIdx.x; i < p.tokens * half; i += kRopeThreads)
-    table[i] = turn_of(pos[i / half], __ldg(p.inv_freq + i % half), p.factor, p.sign);
-}
-__device__ __forceinline__ void load_turns(const float2 *table, int token, const Place &at, const RopeParams &p, float *c,
-                                           float *s) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float2 t = at.turns ? table[token * (p.rotary >> 1) + 8 * at.lane + e] : make_float2(1.f, 0.f);
-    c[e] = t.x;
-    s[e] = t.y;
-  }
-}
-
-template <bool BF, bool NORM, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+// The backward pass with norms.  With dy the upstream gradient turned back, xh = x rstd and
+// g = dy w:   dx = rstd (g - xh mean(g xh)),   dw += dy xh.  Each block leaves its part of the
+// weights' gradients in parts[block][q, k][d], which rope_dw_kernel adds up in a fixed order.
+template <bool BF, bool INTER, int E>
+__global__ void __launch_bounds__(kRopeThreads, E == 8 ? LBB : 1) rope_bwd_kernel(const RopeParams p) {
+  constexpr int U = kBwdAtOnce<E>;
   extern __shared__ float2 turns[];
   __shared__ int pos[kRopeMaxTokens];
+  __shared__ Frequencies freq;
+  __shared__ __align__(16) float weights[1024];
+  __shared__ float red[kRopeThreads / 32][512];
   grid_launch_dependents();
   grid_wait_prior();
-  const int lpr = p.d >> 4, rows = kRopeThreads / lpr, groups = rows / p.tokens;
-  const long long n0 = static_cast<long long>(blockIdx.x) * p.tokens, N = static_cast<long long>(p.B) * p.L;
-  if (threadIdx.x < p.tokens) {
-    const long long n = n0 + threadIdx.x;
-    int x = 0;
-    if (n < N) x = p.positions ? p.positions[(n / p.L) * p.pos_s + n % p.L] : static_cast<int>(n % p.L);
-    pos[threadIdx.x] = x;
-  }
-  __syncthreads();
-  fill_turns(turns, pos, p);
-  __syncthreads();
-  const Place at = place_of<INTER>(p, lpr);
+  const int lpr = p.d / E, groups = kRopeThreads / lpr / p.tokens;
+  const Place at = place_of<INTER, E>(p, lpr);
   const int row = threadIdx.x / lpr, token = row / groups, group = row - token * groups;
-  float c[8], s[8];
-  load_turns(turns, token, at, p, c, s);
-  const long long n = n0 + token;
-  const bool valid = n < N;
-  const long long b = valid ? n / p.L : 0, l = valid ? n % p.L : 0;
-  const int h0 = blockIdx.y * p.heads_per_block, h1 = min(p.Hq + p.Hkv, h0 + p.heads_per_block);
+  const uint32_t out_h = static_cast<uint32_t>(p.L) * static_cast<uint32_t>(p.d);
   const float inv_d = 1.f / static_cast<float>(p.d);
-  const long long out_h = static_cast<long long>(p.L) * p.d;
-  rope_heads<BF, NORM, INTER>(static_cast<const uint16_t *>(p.q) + b * p.qs[0] + l * p.qs[2], p.qs[1],
-                              static_cast<uint16_t *>(p.q_out) + b * p.Hq * out_h + l * p.d, out_h, h0, min(h1, p.Hq), group,
-                              groups, valid, at, lpr, c, s, static_cast<const uint16_t *>(p.q_w), p.eps, inv_d);
-  rope_heads<BF, NORM, INTER>(static_cast<const uint16_t *>(p.k) + b * p.ks[0] + l * p.ks[2], p.ks[1],
-                              static_cast<uint16_t *>(p.k_out) + b * p.Hkv * out_h + l * p.d, out_h, max(h0 - p.Hq, 0),
-                              h1 - p.Hq, group, groups, valid, at, lpr, c, s, static_cast<const uint16_t *>(p.k_w), p.eps, inv_d);
-}
-
-// The append: sequence b's new tokens are counts[b] rows (all L without counts) at positions
-// lengths[b] - counts[b] .. lengths[b] - 1; their keys (turned when rotary > 0) and values go
-// to the pages that the table names, their queries to q_out (zeros behind the last token).
-template <bool BF, bool NORM, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) append_kernel(const RopeParams p) {
-  extern __shared__ float2 turns[];
-  __shared__ int pos[kRopeMaxTokens];
-  __shared__ long long cell[kRopeMaxTokens];  // element offset of the token's page slot, -1: none, -2: behind the last token
-  grid_launch_dependents();
-  grid_wait_prior();
-  const int lpr = p.d >> 4, rows = kRopeThreads / lpr, groups = rows / p.tokens;
-  const long long n0 = static_cast<long long>(blockIdx.x) * p.tokens, N = static_cast<long long>(p.B) * p.L;
-  if (threadIdx.x < p.tokens) {
-    const long long n = n0 + threadIdx.x;
-    int x = 0;
-    long long at = -2;
-    if (n < N) {
-      const long long b = n / p.L;
-      const int t = static_cast<int>(n % p.L);
-      const int len = p.lengths[b], count = p.counts ? p.counts[b] : p.L;
-      if (count < 0 || count > p.L || len < count || len > static_cast<long long>(p.table_w) * p.page) {
-        atomicCAS(p.status, 0u, kDevBadLength);
-      } else if (t < count) {
-        x = len - count + t;
-        const int page = p.table[b * p.table_s + x / p.page];
-        at = -1;
-        if (page < 0 || page >= p.pages)
-          atomicCAS(p.status, 0u, kDevBadPage);
-        else
-          at = page * p.page_s + static_cast<long long>(x % p.page) * p.slot_s;
-      }
-    }
-    pos[threadIdx.x] = x;
-    cell[threadIdx.x] = at;
-  }
-  __syncthreads();
-  fill_turns(turns, pos, p);
-  __syncthreads();
-  const Place at = place_of<INTER>(p, lpr);
-  const int row = threadIdx.x / lpr, token = row / groups, group = row - token * groups;
-  float c[8], s[8];
-  load_turns(turns, token, at, p, c, s);
-  const long long n = n0 + token, to = cell[token];
-  const bool in = n < N;
-  const long long b = in ? n / p.L : 0, l = in ? n % p.L : 0;
-  const int h0 = blockIdx.y * p.heads_per_block, h1 = min(p.Hq + 2 * p.Hkv, h0 + p.heads_per_block);
-  const float inv_d = 1.f / static_cast<float>(p.d);
-  if (p.Hq) {
-    const long long out_h = static_cast<long long>(p.L) * p.d;
-    uint16_t *const out = static_cast<uint16_t *>(p.q_out) + b * p.Hq * out_h + l * p.d;
-    const int e1 = min(h1, p.Hq);
-    if (in && to == -2)
-      for (int h = h0 + group; h < e1; h += groups) {
-        store16(out + h * out_h + at.c0, make_uint4(0, 0, 0, 0));
-        store16(out + h * out_h + at.c1, make_uint4(0, 0, 0, 0));
-      }
-    rope_heads<BF, NORM, INTER>(static_cast<const uint16_t *>(p.q) + b * p.qs[0] + l * p.qs[2], p.qs[1], out, out_h, h0, e1,
-                                group, groups, in && to != -2, at, lpr, c, s, static_cast<const uint16_t *>(p.q_w), p.eps, inv_d);
-  }
-  const bool valid = in && to >= 0;
-  const int k0 = max(h0 - p.Hq, 0), k1 = min(h1 - p.Hq, p.Hkv);
-  const int v0 = max(h0 - p.Hq - p.Hkv, 0), v1 = h1 - p.Hq - p.Hkv;
-  const uint16_t *const ksrc = static_cast<const uint16_t *>(p.k) + b * p.ks[0] + l * p.ks[2];
-  const uint16_t *const vsrc = static_cast<const uint16_t *>(p.v) + b * p.vs[0] + l * p.vs[2];
-  uint16_t *const kdst = static_cast<uint16_t *>(p.k_pages) + (valid ? to : 0);
-  uint16_t *const vdst = static_cast<uint16_t *>(p.v_pages) + (valid ? to : 0);
-  if (NORM || p.rotary) {
-    rope_heads<BF, NORM, INTER>(ksrc, p.ks[1], kdst, p.head_s, k0, k1, group, groups, valid, at, lpr, c, s,
-                                static_cast<const uint16_t *>(p.k_w), p.eps, inv_d);
-  } else if (valid) {
-    for (int h = k0 + group; h < k1; h += groups) {
-      store16(kdst + h * p.head_s + at.c0, load16(ksrc + h * p.ks[1] + at.c0));
-      store16(kdst + h * p.head_s + at.c1, load16(ksrc + h * p.ks[1] + at.c1));
-    }
-  }
-  if (valid)
-    for (int h = v0 + group; h < v1; h += groups) {
-      store16(vdst + h * p.head_s + at.c0, load16(vsrc + h * p.vs[1] + at.c0));
-      store16(vdst + h * p.head_s + at.c1, load16(vsrc + h * p.vs[1] + at.c1));
-    }
-}
-
-// Backward rows of heads [h0, h1): with dy the upstream gradient turned back, xh = x rstd and
-// g = dy w,   dx = rstd (g - xh mean(g xh)),   dw += dy xh  (this thread's 16 columns).
-template <bool BF, bool INTER>
-__device__ __forceinline__ void rope_heads_bwd(const uint16_t *dz, long long dz_h, const uint16_t *src, long long src_h,
-                                               uint16_t *dst, long long dst_h, int h0, int h1, int group, int groups,
-                                               bool valid, const Place &at, int lpr, const float *c, const float *s,
-                                               const uint16_t *weight, float eps, float inv_d, float *dw) {
-  if (h0 >= h1) return;
-  float w[16];
-  vec_unpack<BF>(load16(weight + at.c0), w);
-  vec_unpack<BF>(load16(weight + at.c1), w + 8);
-  constexpr int U = 2;
-  for (int base = h0; base < h1; base += groups * U) {
-    uint4 a[U], b[U], da[U], db[U];
+  fill_weights<BF, INTER, E>(weights, p);
+  fill_frequencies(freq, p);
+  Pairs<E> dwq, dwk;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = base + u * groups + group;
-      a[u] = b[u] = da[u] = db[u] = make_uint4(0, 0, 0, 0);
-      if (valid && h < h1) {
-        a[u] = load16(src + h * src_h + at.c0);
-        b[u] = load16(src + h * src_h + at.c1);
-        da[u] = load16(dz + h * dz_h + at.c0);
-        db[u] = load16(dz + h * dz_h + at.c1);
+  for (int e = 0; e < E / 4; ++e) dwq.A[e] = dwq.B[e] = dwk.A[e] = dwk.B[e] = 0ull;  // pairs of 0.0f
+  Units u = units_of(p);
+  bool fresh = true;
+  Token tok;
+  Turn<E> turn;
+  for (; u.left > 0; --u.left) {
+    const long long n0 = u.tile * p.tokens;
+    if (fresh) tok = token_of(p, n0 + token);
+    const bool is_q = u.step < p.steps_q;
+    const int heads = is_q ? p.Hq : p.Hkv;
+    const int h0 = (u.step - (is_q ? 0 : p.steps_q)) * groups * p.at_once + group;
+    const long long *const xs = is_q ? p.qs : p.ks, *const us = is_q ? p.dqs : p.dks;
+    const uint32_t x_h = static_cast<uint32_t>(xs[1]), up_h = static_cast<uint32_t>(us[1]);
+    const uint16_t *const src = row_at(is_q ? p.q : p.k, tok, xs) + static_cast<uint64_t>(h0) * x_h;
+    const uint16_t *const up = row_at(is_q ? p.dq : p.dk, tok, us) + static_cast<uint64_t>(h0) * up_h;
+    const int rows_here = tok.in && h0 < heads ? min(p.at_once, (heads - h0 + groups - 1) / groups) : 0;  // of this thread
+    Vec<E> a[U], b[U], da[U], db[U];
+    {
+      const uint64_t step = static_cast<uint64_t>(groups) * x_h, up_step = static_cast<uint64_t>(groups) * up_h;
+      const uint16_t *from = src, *grad = up;
+#pragma unroll
+      for (int i = 0; i < U; ++i, from += step, grad += up_step) {
+        a[i] = b[i] = da[i] = db[i] = zero_vec<E>();
+        if (i < rows_here) {
+          a[i] = load_vec<E>(from + at.c0);
+          b[i] = load_vec<E>(from + at.c1);
+          da[i] = load_vec<E>(grad + at.c0);
+          db[i] = load_vec<E>(grad + at.c1);
+        }
       }
+    }
+    if (fresh) {
+      fresh = false;
+      __syncthreads();
+      if (threadIdx.x < p.tokens) {
+        const Token t = token_of(p, n0 + threadIdx.x);
+        pos[threadIdx.x] = !t.in ? 0 : p.positions ? p.positions[t.b * p.pos_s + t.l] : static_cast<int>(t.l);
+      }
+      __syncthreads();
+      if (p.rotary > 0) {
+        fill_turns(turns, pos, freq, p);
+        __syncthreads();
+      }
+      load_turns<E>(turns, token, p.tokens, at, turn);
+    }
+    uint16_t *dst = static_cast<uint16_t *>(is_q ? p.q_out : p.k_out) + tok.b * heads * static_cast<long long>(out_h) +
+                          tok.l * p.d + static_cast<uint64_t>(h0) * out_h;
+    Pairs<E> w, dw;
+    weight_pairs<E>(weights + (is_q ? 0 : p.d), at.lane, w);
+#pragma unroll
+    for (int e = 0; e < E / 4; ++e) dw.A[e] = dw.B[e] = 0ull;
+    const uint64_t step = static_cast<uint64_t>(groups) * out_h;
+    Pairs<E> x[U], g[U];
+    float ss[U], gx[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      unpack<BF, INTER, E>(a[i], b[i], x[i]);
+      unpack<BF, INTER, E>(da[i], db[i], g[i]);
+    }
+    if (at.turns)
+#pragma unroll
+      for (int i = 0; i < U; ++i) turn_pairs<E>(g[i], turn);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      Pairs<E> gw;
+#pragma unroll
+      for (int e = 0; e < E / 4; ++e) {
+        gw.A[e] = fmul2(g[i].A[e], w.A[e]);
+        gw.B[e] = fmul2(g[i].B[e], w.B[e]);
+      }
+      ss[i] = lane_dot<E>(x[i], x[i]);
+      gx[i] = lane_dot<E>(gw, x[i]);
+    }
+    for (int o = 1; o < lpr; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], o);
+        gx[i] += __shfl_xor_sync(0xffffffffu, gx[i], o);
+      }
+#pragma unroll
+    for (int i = 0; i < U; ++i, dst += step) {
+      const float rstd = rsqrtf(ss[i] * inv_d + p.eps);
+      const float mean = gx[i] * rstd * inv_d;  // mean(g xh)
+      const uint64_t r = f32x2(rstd, rstd), m = f32x2(-mean, -mean);
+#pragma unroll
+      for (int e = 0; e < E / 4; ++e) {
+        const uint64_t ha = fmul2(x[i].A[e], r), hb = fmul2(x[i].B[e], r);
+        dw.A[e] = ffma2(g[i].A[e], ha, dw.A[e]);
+        dw.B[e] = ffma2(g[i].B[e], hb, dw.B[e]);
+        x[i].A[e] = fmul2(r, ffma2(ha, m, fmul2(g[i].A[e], w.A[e])));
+        x[i].B[e] = fmul2(r, ffma2(hb, m, fmul2(g[i].B[e], w.B[e])));
+      }
+      if (i < rows_here) store_row<BF, INTER, E>(dst, at, x[i]);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = base + u * groups + group;
-      float x[16], g[16];
-      vec_unpack<BF>(a[u], x);
-      vec_unpack<BF>(b[u], x + 8);
-      vec_unpack<BF>(da[u], g);
-      vec_unpack<BF>(db[u], g + 8);
-      if (at.turns) turn_pairs<INTER>(g, c, s);
-      float ss = 0.f, gx = 0.f;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        ss = fmaf(x[e], x[e], ss);
-        gx = fmaf(g[e] * w[e], x[e], gx);
+    for (int e = 0; e < E / 4; ++e)
+      if (is_q) {
+        dwq.A[e] = fadd2(dwq.A[e], dw.A[e]);
+        dwq.B[e] = fadd2(dwq.B[e], dw.B[e]);
+      } else {
+        dwk.A[e] = fadd2(dwk.A[e], dw.A[e]);
+        dwk.B[e] = fadd2(dwk.B[e], dw.B[e]);
       }
-      ss = row_sum(ss, lpr);
-      gx = row_sum(gx, lpr);
-      const float rstd = rsqrtf(ss * inv_d + eps);
-      const float mean = gx * rstd * inv_d;  // mean(g xh)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float xh = x[e] * rstd;
-        dw[e] = fmaf(g[e], xh, dw[e]);
-        x[e] = rstd * (g[e] * w[e] - xh * mean);
-      }
-      if (valid && h < h1) {
-        store16(dst + h * dst_h + at.c0, vec_pack<BF>(x));
-        store16(dst + h * dst_h + at.c1, vec_pack<BF>(x + 8));
-      }
+    if (++u.step == p.steps) {
+      u.step = 0;
+      ++u.tile;
+      fresh = true;
     }
-  }
-}
-
-// Blocks walk over token tiles; each leaves its part of the weights' gradients in
-// parts[block][q, k][d], which rope_dw_kernel adds up in a fixed order.
-template <bool BF, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_bwd_kernel(const RopeParams p) {
-  extern __shared__ float2 turns[];
-  __shared__ int pos[kRopeMaxTokens];
-  __shared__ float red[8][512];
-  grid_launch_dependents();
-  grid_wait_prior();
-  const int lpr = p.d >> 4, rows = kRopeThreads / lpr, groups = rows / p.tokens;
-  const long long N = static_cast<long long>(p.B) * p.L;
-  const Place at = place_of<INTER>(p, lpr);
-  const int row = threadIdx.x / lpr, token = row / groups, group = row - token * groups;
-  const int h0 = blockIdx.y * p.heads_per_block, h1 = min(p.Hq + p.Hkv, h0 + p.heads_per_block);
-  const float inv_d = 1.f / static_cast<float>(p.d);
-  const long long out_h = static_cast<long long>(p.L) * p.d;
-  float dwq[16], dwk[16];
-#pragma unroll
-  for (int e = 0; e < 16; ++e) dwq[e] = dwk[e] = 0.f;
-  for (long long n0 = static_cast<long long>(blockIdx.x) * p.tokens; n0 < N; n0 += static_cast<long long>(gridDim.x) * p.tokens) {
-    __syncthreads();
-    if (threadIdx.x < p.tokens) {
-      const long long n = n0 + threadIdx.x;
-      int x = 0;
-      if (n < N) x = p.positions ? p.positions[(n / p.L) * p.pos_s + n % p.L] : static_cast<int>(n % p.L);
-      pos[threadIdx.x] = x;
-    }
-    __syncthreads();
-    fill_turns(turns, pos, p);
-    __syncthreads();
-    float c[8], s[8];
-    load_turns(turns, token, at, p, c, s);
-    const long long n = n0 + token;
-    const bool valid = n < N;
-    const long long b = valid ? n / p.L : 0, l = valid ? n % p.L : 0;
-    rope_heads_bwd<BF, INTER>(static_cast<const uint16_t *>(p.dq) + b * p.dqs[0] + l * p.dqs[2], p.dqs[1],
-                              static_cast<const uint16_t *>(p.q) + b * p.qs[0] + l * p.qs[2], p.qs[1],
-                              static_cast<uint16_t *>(p.q_out) + b * p.Hq * out_h + l * p.d, out_h, h0, min(h1, p.Hq), group,
-                              groups, valid, at, lpr, c, s, static_cast<const uint16_t *>(p.q_w), p.eps, inv_d, dwq);
-    rope_heads_bwd<BF, INTER>(static_cast<const uint16_t *>(p.dk) + b * p.dks[0] + l * p.dks[2], p.dks[1],
-                              static_cast<const uint16_t *>(p.k) + b * p.ks[0] + l * p.ks[2], p.ks[1],
-                              static_cast<uint16_t *>(p.k_out) + b * p.Hkv * out_h + l * p.d, out_h, max(h0 - p.Hq, 0), h1 - p.Hq,
-                              group, groups, valid, at, lpr, c, s, static_cast<const uint16_t *>(p.k_w), p.eps, inv_d, dwk);
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float *const part = p.parts + (static_cast<size_t>(blockIdx.y) * gridDim.x + blockIdx.x) * 2 * p.d;
+  float *const part = p.parts + static_cast<size_t>(blockIdx.x) * 2 * p.d;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
-    float *const dw = which ? dwk : dwq;
+    const Pairs<E> &acc = which ? dwk : dwq;
+    float dw[E];
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
+    for (int e = 0; e < E / 4; ++e) {
+      f32x2_split(acc.A[e], dw[2 * e], dw[2 * e + 1]);
+      f32x2_split(acc.B[e], dw[E / 2 + 2 * e], dw[E / 2 + 2 * e + 1]);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e)
       for (int o = lpr; o < 32; o <<= 1) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], o);
     __syncthreads();
     if (lane < lpr) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        red[warp][at.c0 + e] = dw[e];
-        red[warp][at.c1 + e] = dw[8 + e];
+      for (int e = 0; e < E; ++e) {  // A's and B's elements in the row
+        const int r = e % (E / 2), half = e / (E / 2);
+        red[warp][INTER ? at.c0 + 2 * r + half : (half ? at.c1 : at.c0) + r] = dw[e];
       }
     }
     __syncthreads();
@@ -434,55 +650,73 @@ cudaError_t launch(void (*kern)(A...), dim3 grid, int threads, size_t smem, cuda
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// Tokens and heads of a block.  As many tokens (a power of two up to 8, so that a head's rows
-// of neighbouring tokens are written together) as still leave two blocks per SM; with fewer
-// tokens than that the heads are split over blocks too.
-dim3 plan(RopeParams &p, int heads, int sm_count, long long max_blocks) {
-  const long long N = static_cast<long long>(p.B) * p.L, want = 2LL * sm_count;
-  p.tokens = kRopeMaxTokens;
-  while (p.tokens > 1 && (N + p.tokens - 1) / p.tokens < want) p.tokens >>= 1;
-  const long long tiles = (N + p.tokens - 1) / p.tokens;
-  const int groups = kRopeThreads / (p.d >> 4) / p.tokens;
-  long long split = std::max(1LL, std::min<long long>(want / tiles, (heads + groups - 1) / groups));
-  p.heads_per_block = static_cast<int>((heads + split - 1) / split);
-  split = (heads + p.heads_per_block - 1) / p.heads_per_block;
-  return dim3(static_cast<unsigned>(std::min(tiles, std::max(1LL, max_blocks / split))), static_cast<unsigned>(split));
+// The units.  A tile's angles are computed by every block that has a unit of it, so a tile gets
+// as many tokens (a power of two) as leave each of `blocks` blocks about one tile, but no fewer
+// than TMIN, whose angles one pass of the block's threads computes anyway, and no more
+// than RT (a head's rows of neighbouring tokens are written together: 32 rows of d = 64 are 4 KB).
+// Fewer rows a thread where that leaves blocks without a unit.  Returns the blocks to launch.
+#ifndef TMIN
+#define TMIN 4
+#endif
+int plan(RopeParams &p, bool append, int blocks, int at_once) {
+  const long long N = static_cast<long long>(p.B) * p.L;
+  const int rows = kRopeThreads / (p.d > 256 ? p.d / 16 : p.d / 8);
+  const int most = std::min(RT, rows);
+  p.tokens = 1;
+  while (2 * p.tokens <= most && (2LL * p.tokens * blocks <= N || (p.tokens < TMIN && p.tokens < N))) p.tokens *= 2;
+  for (p.at_once = at_once;; p.at_once >>= 1) {
+    const int per = rows / p.tokens * p.at_once;
+    p.steps_q = (p.Hq + per - 1) / per;
+    p.steps_k = (p.Hkv + per - 1) / per;
+    p.steps = p.steps_q + (append ? 2 : 1) * p.steps_k;
+    p.units = (N + p.tokens - 1) / p.tokens * p.steps;
+    if (p.at_once == 1 || p.units >= blocks) break;
+  }
+  return static_cast<int>(std::min<long long>(p.units, blocks));
 }
 
 size_t turns_bytes(const RopeParams &p) { return static_cast<size_t>(p.tokens) * (p.rotary / 2) * sizeof(float2); }
 
-constexpr long long kNoCap = 1LL << 40;
+// The instance for a call's type, norm, layout and head_dim.
+template <bool APPEND>
+auto pick(bool bf, bool norm, bool inter, int d) {
+#define ROPE_PICK(E)                                                                                                         \
+  (bf ? (norm ? (inter ? rope_kernel<true, true, true, E, APPEND> : rope_kernel<true, true, false, E, APPEND>)               \
+              : (inter ? rope_kernel<true, false, true, E, APPEND> : rope_kernel<true, false, false, E, APPEND>))            \
+      : (norm ? (inter ? rope_kernel<false, true, true, E, APPEND> : rope_kernel<false, true, false, E, APPEND>)             \
+              : (inter ? rope_kernel<false, false, true, E, APPEND> : rope_kernel<false, false, false, E, APPEND>)))
+  return d > 256 ? ROPE_PICK(16) : ROPE_PICK(8);
+#undef ROPE_PICK
+}
+auto pick_bwd(bool bf, bool inter, int d) {
+#define ROPE_PICK(E)                                                                   \
+  (bf ? (inter ? rope_bwd_kernel<true, true, E> : rope_bwd_kernel<true, false, E>)     \
+      : (inter ? rope_bwd_kernel<false, true, E> : rope_bwd_kernel<false, false, E>))
+  return d > 256 ? ROPE_PICK(16) : ROPE_PICK(8);
+#undef ROPE_PICK
+}
+
+template <bool APPEND>
+cudaError_t launch_rows(RopeLaunch &a) {
+  const bool norm = a.p.q_w != nullptr || a.p.k_w != nullptr;
+  const int E = a.p.d > 256 ? 16 : 8;
+  const int grid = plan(a.p, APPEND, a.sm_count * rope_resident(E, norm), (E == 16 ? kAtOnce<16> : kAtOnce<8>));
+  return launch(pick<APPEND>(a.bf16, norm, a.interleaved, a.p.d), dim3(grid), kRopeThreads, turns_bytes(a.p), a.stream, RopeParams(a.p));
+}
 
 }  // namespace
 
-cudaError_t launch_rope(RopeLaunch &a) {
-  const dim3 grid = plan(a.p, a.p.Hq + a.p.Hkv, a.sm_count, kNoCap);
-  const bool norm = a.p.q_w != nullptr;
-  auto *kern = a.bf16 ? (norm ? (a.interleaved ? rope_kernel<true, true, true> : rope_kernel<true, true, false>)
-                              : (a.interleaved ? rope_kernel<true, false, true> : rope_kernel<true, false, false>))
-                      : (norm ? (a.interleaved ? rope_kernel<false, true, true> : rope_kernel<false, true, false>)
-                              : (a.interleaved ? rope_kernel<false, false, true> : rope_kernel<false, false, false>));
-  return launch(kern, grid, kRopeThreads, turns_bytes(a.p), a.stream, RopeParams(a.p));
-}
-
-cudaError_t launch_append(RopeLaunch &a) {
-  const dim3 grid = plan(a.p, a.p.Hq + 2 * a.p.Hkv, a.sm_count, kNoCap);
-  const bool norm = a.p.q_w != nullptr || a.p.k_w != nullptr;
-  auto *kern = a.bf16 ? (norm ? (a.interleaved ? append_kernel<true, true, true> : append_kernel<true, true, false>)
-                              : (a.interleaved ? append_kernel<true, false, true> : append_kernel<true, false, false>))
-                      : (norm ? (a.interleaved ? append_kernel<false, true, true> : append_kernel<false, true, false>)
-                              : (a.interleaved ? append_kernel<false, false, true> : append_kernel<false, false, false>));
-  return launch(kern, grid, kRopeThreads, turns_bytes(a.p), a.stream, RopeParams(a.p));
-}
+cudaError_t launch_rope(RopeLaunch &a) { return launch_rows<false>(a); }
+cudaError_t launch_append(RopeLaunch &a) { return launch_rows<true>(a); }
 
 cudaError_t launch_rope_bwd(RopeLaunch &a) {
-  const dim3 grid = plan(a.p, a.p.Hq + a.p.Hkv, a.sm_count, std::min<long long>(kRopeMaxParts, 4LL * a.sm_count));
-  auto *kern = a.bf16 ? (a.interleaved ? rope_bwd_kernel<true, true> : rope_bwd_kernel<true, false>)
-                      : (a.interleaved ? rope_bwd_kernel<false, true> : rope_bwd_kernel<false, false>);
-  const cudaError_t e = launch(kern, grid, kRopeThreads, turns_bytes(a.p), a.stream, RopeParams(a.p));
+  const int E = a.p.d > 256 ? 16 : 8, resident = E == 16 ? 1 : LBB;
+  const int grid = plan(a.p, false, std::min(kRopeMaxParts, a.sm_count * resident), (E == 16 ? kBwdAtOnce<16> : kBwdAtOnce<8>));
+  const cudaError_t e =
+      launch(pick_bwd(a.bf16, a.interleaved, a.p.d), dim3(grid), kRopeThreads, turns_bytes(a.p), a.stream, RopeParams(a.p));
   if (e != cudaSuccess) return e;
-  return launch(rope_dw_kernel, dim3(a.p.d / 32, a.p.k_w ? 2 : 1), 1024, 0, a.stream, static_cast<const float *>(a.p.parts),
-                static_cast<int>(grid.x * grid.y), a.p.d, a.p.dq_w, a.p.dk_w);
+  return launch(rope_dw_kernel, dim3(a.p.d / 32, a.p.k_w ? 2 : 1), 1024, 0, a.stream, static_cast<const float *>(a.p.parts), grid, a.p.d,
+                a.p.dq_w, a.p.dk_w);
 }
 
 }  // namespace gbattn

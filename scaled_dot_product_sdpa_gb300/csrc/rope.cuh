@@ -17,7 +17,7 @@ namespace gbattn {
 constexpr unsigned kDevBadPage = 8;    // a page number outside the cache within a sequence's length
 constexpr unsigned kDevBadLength = 9;  // a length that is negative or beyond the page table
 constexpr int kRopeThreads = 256;
-constexpr int kRopeMaxTokens = 8;      // tokens a block works on at once
+constexpr int kRopeMaxTokens = 32;     // tokens a block works on at once
 constexpr int kRopeMaxParts = 640;     // partial weight gradients (blocks) of the backward pass
 
 struct RopeParams {
@@ -34,8 +34,10 @@ struct RopeParams {
   const void *q_w, *k_w;             // [d] norm weights, or null
   float eps, factor, sign;           // sign -1 turns backwards
   int B, Hq, Hkv, L, d, rotary;
-  int tokens;                        // per block: 1, 2, 4 or 8
-  int heads_per_block;               // of the concatenated head list (q, k, v)
+  int tokens;                        // per block: a power of two up to kRopeMaxTokens
+  int at_once;                       // rows of a unit that each thread works on
+  int steps, steps_q, steps_k;       // units of a tile: all, of q, of k (and of v)
+  long long units;                   // in all
   // append
   void *k_pages, *v_pages;           // [pages, Hkv, page, d] by strides
   long long page_s, head_s, slot_s;

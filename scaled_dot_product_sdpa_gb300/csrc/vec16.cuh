@@ -1,4 +1,4 @@
-// vec16.cuh -- 16-byte vectors of eight fp16 or bf16 values as fp32 and back (to nearest even).
+// vec16.cuh -- pairs of fp16 or bf16 values as fp32, and back (to nearest even).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -9,18 +9,14 @@
 namespace gbattn {
 
 template <bool BF>
-__device__ __forceinline__ void vec_unpack(const uint4 &u, float *f) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (BF) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    } else {
-      const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-      f[2 * i] = t.x;
-      f[2 * i + 1] = t.y;
-    }
+__device__ __forceinline__ void unpack2(uint32_t w, float &lo, float &hi) {
+  if constexpr (BF) {
+    lo = __uint_as_float(w << 16);
+    hi = __uint_as_float(w & 0xffff0000u);
+  } else {
+    const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    lo = t.x;
+    hi = t.y;
   }
 }
 
@@ -32,11 +28,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   else
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
-}
-
-template <bool BF>
-__device__ __forceinline__ uint4 vec_pack(const float *f) {
-  return make_uint4(pack2<BF>(f[0], f[1]), pack2<BF>(f[2], f[3]), pack2<BF>(f[4], f[5]), pack2<BF>(f[6], f[7]));
 }
 
 }  // namespace gbattn
