@@ -9,13 +9,17 @@
 // and in both layouts lane j turns its pairs by the angles E/2 j .. E/2 j + E/2 - 1.  The norm's
 // sum of squares is a shuffle reduction over the row's lanes.
 //
-// The work is cut into units, `at_once` rows for each thread: a tile of `tokens` consecutive
-// (batch, row) positions times a run of heads of the joint list (q, k and, for the append, v).
-// As many blocks as fit the GPU at once take equal runs of consecutive units, so that none is
-// left with a thin last wave (1024 blocks of a tile each, three to an SM, took 44.7 us for
-// norm and rotation of 4 x 40 x 2048 x 128 in bf16).  A unit's loads are all issued before its
-// first row is worked on; a new tile's cosines and sines are computed once, into shared
-// memory, behind them, and each thread keeps those of its token in registers.
+// The work is cut into units, a few rows for each thread: a tile of `tokens` consecutive (batch,
+// row) positions times a run of heads of one tensor (q, k or, for the append, v).  As many blocks
+// as fit the GPU at once take equal runs of consecutive units, so that none is left with a thin
+// last wave.  A unit's loads are all issued before its first row is worked on; a new tile's
+// cosines and sines are computed once, into shared memory, behind them, and each thread keeps
+// those of its token in registers.  Arithmetic runs on fp32 pairs (two elements an instruction):
+// with 16 elements a lane and scalar arithmetic, norm and rotation of 4 x 40 x 2048 x 128 in bf16
+// took 44.5 us on GB300 and its backward pass 92 (registers for 2 to 4 warps a scheduler, 180
+// instructions for two rows); now 37.8 (4.5 TB/s) and 63.6 (4.0 TB/s), rotation alone of 100003 x
+// 32 x 64 136 us (6.0 TB/s).  What bounds the norms now is the latency of their chain, loads,
+// reduction, stores, at 24 warps an SM.
 //
 // Angles: position x inv_freq is reduced in integers.  inv_freq / 2 pi becomes a 64-bit
 // binary fraction of a turn; its product with the position, taken modulo 2^64, is the angle
@@ -27,38 +31,21 @@
 #include "rope.cuh"
 #include "vec16.cuh"
 
-#ifndef AO
-#define AO 4
-#endif
-#ifndef LB
-#define LB 3
-#endif
-#ifndef LBN
-#define LBN 3
-#endif
-#ifndef BU
-#define BU 2
-#endif
-#ifndef LBB
-#define LBB 3
-#endif
-#ifndef RT
-#define RT 32
-#endif
-#ifndef RB
-#define RB 4
-#endif
-
 namespace gbattn {
 namespace {
 
-// Rows that a thread loads before it works on the first.
+// Rows that a thread loads before it works on the first, and blocks that share an SM (the
+// kernels' launch bounds).  Measured on GB300 with 4 rows and 3 blocks against 2 rows and 4 blocks:
+// rotation of 8 x 64 x 512 x 128 26.7 us, 32.3; with norms of 4 x 40 x 2048 x 128 37.8, 46.5.  The
+// backward pass reads twice as much a row: 4 rows and 2 blocks 63.6 us, 2 rows and 3 blocks 70.2.
 template <int E>
-constexpr int kAtOnce = E == 8 ? AO : 2;
+constexpr int kAtOnce = E == 8 ? 4 : 2;
 template <int E>
-constexpr int kBwdAtOnce = E == 8 ? BU : 1;
-// Blocks that share an SM (the kernels' launch bounds).
-constexpr int rope_resident(int E, bool norm) { return E == 16 ? 2 : norm ? LBN : LB; }
+constexpr int kResident = E == 8 ? 3 : 2;
+template <int E>
+constexpr int kBwdAtOnce = E == 8 ? 4 : 1;
+template <int E>
+constexpr int kBwdResident = E == 8 ? 2 : 1;
 
 // frac(x / 2 pi) 2^64 of a finite double x = m 2^e (m an integer of at most 53 bits):
 // m C 2^(e - 2) with C = 2^66 / 2 pi, as a 128-bit integer, modulo 2^64.
@@ -284,12 +271,21 @@ __device__ __forceinline__ void load_turns(const float2 *table, int token, int t
 // The units of this block, as a run over tiles and steps; a step is a run of heads of one tensor.
 struct Units {
   long long tile;
-  int step;
+  int step, stride;  // stride: from tile to tile
   long long left;
 };
 __device__ __forceinline__ Units units_of(const RopeParams &p) {
-  const long long u0 = p.units * blockIdx.x / gridDim.x, u1 = p.units * (blockIdx.x + 1) / gridDim.x;
   Units u;
+  if (p.scattered) {  // whole tiles, gridDim.x apart
+    const long long tiles = p.units / p.steps;
+    u.tile = blockIdx.x;
+    u.step = 0;
+    u.stride = gridDim.x;
+    u.left = (tiles - blockIdx.x + gridDim.x - 1) / gridDim.x * p.steps;
+    return u;
+  }
+  const long long u0 = p.units * blockIdx.x / gridDim.x, u1 = p.units * (blockIdx.x + 1) / gridDim.x;
+  u.stride = 1;
   u.tile = u0 / p.steps;
   u.step = static_cast<int>(u0 - u.tile * p.steps);
   u.left = u1 - u0;
@@ -309,8 +305,8 @@ __device__ __forceinline__ Token token_of(const RopeParams &p, long long n) {
   t.l = t.in ? n - static_cast<long long>(b) * p.L : 0;
   return t;
 }
-__device__ __forceinline__ const uint16_t *row_at(const void *p, const Token &t, const long long *strides) {
-  return static_cast<const uint16_t *>(p) + t.b * strides[0] + t.l * strides[2];
+__device__ __forceinline__ const uint16_t *row_at(const void *p, const Token &t, long long batch, long long row) {
+  return static_cast<const uint16_t *>(p) + t.b * batch + t.l * row;
 }
 
 // attn_rope and (APPEND) attn_cache_append.  The append's new tokens of sequence b are counts[b]
@@ -318,7 +314,7 @@ __device__ __forceinline__ const uint16_t *row_at(const void *p, const Token &t,
 // and values go to the pages that the table names, their queries to q_out (zeros behind the
 // last token).
 template <bool BF, bool NORM, bool INTER, int E, bool APPEND>
-__global__ void __launch_bounds__(kRopeThreads, E == 16 ? 2 : NORM ? LBN : LB) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kResident<E>) rope_kernel(const RopeParams p) {
   constexpr int U = kAtOnce<E>;
   extern __shared__ float2 turns[];
   __shared__ int pos[kRopeMaxTokens];
@@ -336,20 +332,26 @@ __global__ void __launch_bounds__(kRopeThreads, E == 16 ? 2 : NORM ? LBN : LB) r
   if constexpr (NORM) fill_weights<BF, INTER, E>(weights, p);
   fill_frequencies(freq, p);
   Units u = units_of(p);
-  bool fresh = true;
+  bool fresh = true, reads = false;
   Token tok;
   long long to = 0;
   Turn<E> turn;
   for (; u.left > 0; --u.left) {
     const long long n0 = u.tile * p.tokens;
-    if (fresh) tok = token_of(p, n0 + token);
+    if (fresh) {
+      tok = token_of(p, n0 + token);
+      reads = tok.in;
+      if constexpr (APPEND)
+        if (p.counts && tok.in) reads = tok.l < p.counts[tok.b];  // rows behind the last token are not read
+    }
     // The unit's tensor, heads and source; the same in every thread but for the token.
     const int kind = u.step < p.steps_q ? 0 : u.step < p.steps_q + p.steps_k ? 1 : 2;
     const int heads = kind == 0 ? p.Hq : p.Hkv;
     const int h0 = (u.step - (kind == 0 ? 0 : kind == 1 ? p.steps_q : p.steps_q + p.steps_k)) * groups * p.at_once + group;
-    const long long *const strides = kind == 0 ? p.qs : kind == 1 ? p.ks : p.vs;
-    const uint32_t src_h = static_cast<uint32_t>(strides[1]);
-    const uint16_t *src = row_at(kind == 0 ? p.q : kind == 1 ? p.k : p.v, tok, strides) + static_cast<uint64_t>(h0) * src_h;
+    const uint32_t src_h = static_cast<uint32_t>(kind == 0 ? p.qs[1] : kind == 1 ? p.ks[1] : p.vs[1]);
+    const uint16_t *src = row_at(kind == 0 ? p.q : kind == 1 ? p.k : p.v, tok, kind == 0 ? p.qs[0] : kind == 1 ? p.ks[0] : p.vs[0],
+                                 kind == 0 ? p.qs[2] : kind == 1 ? p.ks[2] : p.vs[2]) +
+                          static_cast<uint64_t>(h0) * src_h;
     const int rows_here = tok.in && h0 < heads ? min(p.at_once, (heads - h0 + groups - 1) / groups) : 0;  // of this thread
     Vec<E> a[U], b[U];
     {
@@ -358,7 +360,7 @@ __global__ void __launch_bounds__(kRopeThreads, E == 16 ? 2 : NORM ? LBN : LB) r
 #pragma unroll
       for (int i = 0; i < U; ++i, from += step) {
         a[i] = b[i] = zero_vec<E>();
-        if (i < rows_here) {
+        if (reads && i < rows_here) {
           a[i] = load_vec<E>(from + at.c0);
           b[i] = load_vec<E>(from + at.c1);
         }
@@ -449,7 +451,7 @@ __global__ void __launch_bounds__(kRopeThreads, E == 16 ? 2 : NORM ? LBN : LB) r
     }
     if (++u.step == p.steps) {
       u.step = 0;
-      ++u.tile;
+      u.tile += u.stride;
       fresh = true;
     }
   }
@@ -459,13 +461,13 @@ __global__ void __launch_bounds__(kRopeThreads, E == 16 ? 2 : NORM ? LBN : LB) r
 // g = dy w:   dx = rstd (g - xh mean(g xh)),   dw += dy xh.  Each block leaves its part of the
 // weights' gradients in parts[block][q, k][d], which rope_dw_kernel adds up in a fixed order.
 template <bool BF, bool INTER, int E>
-__global__ void __launch_bounds__(kRopeThreads, E == 8 ? LBB : 1) rope_bwd_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kBwdResident<E>) rope_bwd_kernel(const RopeParams p) {
   constexpr int U = kBwdAtOnce<E>;
   extern __shared__ float2 turns[];
   __shared__ int pos[kRopeMaxTokens];
   __shared__ Frequencies freq;
   __shared__ __align__(16) float weights[1024];
-  __shared__ float red[kRopeThreads / 32][512];
+  __shared__ float sums[2][E][kRopeThreads];  // each thread's part of q's and k's weight gradients
   grid_launch_dependents();
   grid_wait_prior();
   const int lpr = p.d / E, groups = kRopeThreads / lpr / p.tokens;
@@ -475,9 +477,25 @@ __global__ void __launch_bounds__(kRopeThreads, E == 8 ? LBB : 1) rope_bwd_kerne
   const float inv_d = 1.f / static_cast<float>(p.d);
   fill_weights<BF, INTER, E>(weights, p);
   fill_frequencies(freq, p);
-  Pairs<E> dwq, dwk;
+  Pairs<E> dw;  // of the tensor that the steps are in
+  auto add_up = [&](int which) {
 #pragma unroll
-  for (int e = 0; e < E / 4; ++e) dwq.A[e] = dwq.B[e] = dwk.A[e] = dwk.B[e] = 0ull;  // pairs of 0.0f
+    for (int e = 0; e < E / 4; ++e) {
+      float f[4];
+      f32x2_split(dw.A[e], f[0], f[1]);
+      f32x2_split(dw.B[e], f[2], f[3]);
+      sums[which][2 * e][threadIdx.x] += f[0];
+      sums[which][2 * e + 1][threadIdx.x] += f[1];
+      sums[which][E / 2 + 2 * e][threadIdx.x] += f[2];
+      sums[which][E / 2 + 2 * e + 1][threadIdx.x] += f[3];
+      dw.A[e] = dw.B[e] = 0ull;  // pairs of 0.0f
+    }
+  };
+#pragma unroll
+  for (int e = 0; e < E; ++e) sums[0][e][threadIdx.x] = sums[1][e][threadIdx.x] = 0.f;
+#pragma unroll
+  for (int e = 0; e < E / 4; ++e) dw.A[e] = dw.B[e] = 0ull;
+  bool last_q = true;
   Units u = units_of(p);
   bool fresh = true;
   Token tok;
@@ -486,12 +504,15 @@ __global__ void __launch_bounds__(kRopeThreads, E == 8 ? LBB : 1) rope_bwd_kerne
     const long long n0 = u.tile * p.tokens;
     if (fresh) tok = token_of(p, n0 + token);
     const bool is_q = u.step < p.steps_q;
+    if (is_q != last_q) add_up(last_q ? 0 : 1);
+    last_q = is_q;
     const int heads = is_q ? p.Hq : p.Hkv;
     const int h0 = (u.step - (is_q ? 0 : p.steps_q)) * groups * p.at_once + group;
-    const long long *const xs = is_q ? p.qs : p.ks, *const us = is_q ? p.dqs : p.dks;
-    const uint32_t x_h = static_cast<uint32_t>(xs[1]), up_h = static_cast<uint32_t>(us[1]);
-    const uint16_t *const src = row_at(is_q ? p.q : p.k, tok, xs) + static_cast<uint64_t>(h0) * x_h;
-    const uint16_t *const up = row_at(is_q ? p.dq : p.dk, tok, us) + static_cast<uint64_t>(h0) * up_h;
+    const uint32_t x_h = static_cast<uint32_t>(is_q ? p.qs[1] : p.ks[1]), up_h = static_cast<uint32_t>(is_q ? p.dqs[1] : p.dks[1]);
+    const uint16_t *const src =
+        row_at(is_q ? p.q : p.k, tok, is_q ? p.qs[0] : p.ks[0], is_q ? p.qs[2] : p.ks[2]) + static_cast<uint64_t>(h0) * x_h;
+    const uint16_t *const up =
+        row_at(is_q ? p.dq : p.dk, tok, is_q ? p.dqs[0] : p.dks[0], is_q ? p.dqs[2] : p.dks[2]) + static_cast<uint64_t>(h0) * up_h;
     const int rows_here = tok.in && h0 < heads ? min(p.at_once, (heads - h0 + groups - 1) / groups) : 0;  // of this thread
     Vec<E> a[U], b[U], da[U], db[U];
     {
@@ -524,10 +545,8 @@ __global__ void __launch_bounds__(kRopeThreads, E == 8 ? LBB : 1) rope_bwd_kerne
     }
     uint16_t *dst = static_cast<uint16_t *>(is_q ? p.q_out : p.k_out) + tok.b * heads * static_cast<long long>(out_h) +
                           tok.l * p.d + static_cast<uint64_t>(h0) * out_h;
-    Pairs<E> w, dw;
+    Pairs<E> w;
     weight_pairs<E>(weights + (is_q ? 0 : p.d), at.lane, w);
-#pragma unroll
-    for (int e = 0; e < E / 4; ++e) dw.A[e] = dw.B[e] = 0ull;
     const uint64_t step = static_cast<uint64_t>(groups) * out_h;
     Pairs<E> x[U], g[U];
     float ss[U], gx[U];
@@ -571,68 +590,43 @@ __global__ void __launch_bounds__(kRopeThreads, E == 8 ? LBB : 1) rope_bwd_kerne
       }
       if (i < rows_here) store_row<BF, INTER, E>(dst, at, x[i]);
     }
-#pragma unroll
-    for (int e = 0; e < E / 4; ++e)
-      if (is_q) {
-        dwq.A[e] = fadd2(dwq.A[e], dw.A[e]);
-        dwq.B[e] = fadd2(dwq.B[e], dw.B[e]);
-      } else {
-        dwk.A[e] = fadd2(dwk.A[e], dw.A[e]);
-        dwk.B[e] = fadd2(dwk.B[e], dw.B[e]);
-      }
     if (++u.step == p.steps) {
       u.step = 0;
-      ++u.tile;
+      u.tile += u.stride;
       fresh = true;
     }
   }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  add_up(last_q ? 0 : 1);
+  __syncthreads();
+  // Lane j's element e (A's, then B's) of every row of threads.
   float *const part = p.parts + static_cast<size_t>(blockIdx.x) * 2 * p.d;
-#pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    const Pairs<E> &acc = which ? dwk : dwq;
-    float dw[E];
-#pragma unroll
-    for (int e = 0; e < E / 4; ++e) {
-      f32x2_split(acc.A[e], dw[2 * e], dw[2 * e + 1]);
-      f32x2_split(acc.B[e], dw[E / 2 + 2 * e], dw[E / 2 + 2 * e + 1]);
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      for (int o = lpr; o < 32; o <<= 1) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], o);
-    __syncthreads();
-    if (lane < lpr) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) {  // A's and B's elements in the row
-        const int r = e % (E / 2), half = e / (E / 2);
-        red[warp][INTER ? at.c0 + 2 * r + half : (half ? at.c1 : at.c0) + r] = dw[e];
-      }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < p.d; i += kRopeThreads) {
-      float t = 0.f;
-#pragma unroll
-      for (int k = 0; k < kRopeThreads / 32; ++k) t += red[k][i];
-      part[which * p.d + i] = t;
-    }
+  for (int i = threadIdx.x; i < 2 * p.d; i += kRopeThreads) {
+    const int which = i >= p.d, k = i - which * p.d, j = k / E, e = k % E, r = e % (E / 2), half = e / (E / 2);
+    float t = 0.f;
+    for (int row_of = 0; row_of < kRopeThreads; row_of += lpr) t += sums[which][e][row_of + j];
+    const bool split = !INTER && j < p.rotary / E;
+    part[which * p.d + (split ? half * (p.rotary >> 1) + E / 2 * j + r : INTER ? E * j + 2 * r + half : E * j + e)] = t;
   }
 }
 
-// dw[which][i] = sum over parts; one block per (which, 32 columns), 32 x 32 threads.
+// dw[which][i] = sum over parts; one block per (which, 16 columns), 16 x 64 threads.
 __global__ void __launch_bounds__(1024) rope_dw_kernel(const float *parts, int n, int d, float *dq_w, float *dk_w) {
-  __shared__ float red[32][33];
+  __shared__ float red[64][17];
   grid_launch_dependents();
   grid_wait_prior();
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, which = blockIdx.y, col = blockIdx.x * 32 + x;
+  const int x = threadIdx.x & 15, y = threadIdx.x >> 4, which = blockIdx.y, col = blockIdx.x * 16 + x;
   float t = 0.f;
-#pragma unroll 4
-  for (int r = y; r < n; r += 32) t += parts[(static_cast<size_t>(r) * 2 + which) * d + col];
+#pragma unroll 8
+  for (int r = y; r < n; r += 64) t += parts[(static_cast<size_t>(r) * 2 + which) * d + col];
   red[y][x] = t;
   __syncthreads();
-  t = red[x][y];
+  if (threadIdx.x < 512) {  // a warp to a column
+    const int lane = threadIdx.x & 31, c = threadIdx.x >> 5;
+    t = red[lane][c] + red[lane + 32][c];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  if (x == 0) (which ? dk_w : dq_w)[blockIdx.x * 32 + y] = t;
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (lane == 0) (which ? dk_w : dq_w)[blockIdx.x * 16 + c] = t;
+  }
 }
 
 template <typename... A>
@@ -651,19 +645,22 @@ cudaError_t launch(void (*kern)(A...), dim3 grid, int threads, size_t smem, cuda
 }
 
 // The units.  A tile's angles are computed by every block that has a unit of it, so a tile gets
-// as many tokens (a power of two) as leave each of `blocks` blocks about one tile, but no fewer
-// than TMIN, whose angles one pass of the block's threads computes anyway, and no more
-// than RT (a head's rows of neighbouring tokens are written together: 32 rows of d = 64 are 4 KB).
-// Fewer rows a thread where that leaves blocks without a unit.  Returns the blocks to launch.
-#ifndef TMIN
-#define TMIN 4
-#endif
+// as many tokens (a power of two) as leave each of `blocks` blocks about one tile (one token a
+// tile took 19.4 us for norm and rotation of 1 x 40 x 2048 x 128 on GB300, four 16.6), but no fewer
+// than four, whose angles one pass of the block's threads computes anyway, and no more than
+// kRopeMaxTokens (a head's rows of neighbouring tokens are written together: 32 rows of d = 64
+// are 4 KB; 100003 x 32 x 64 136.6 us, with 16 tokens 142.2).  Fewer rows a thread where that
+// leaves blocks without a unit.  Returns the blocks to launch.
 int plan(RopeParams &p, bool append, int blocks, int at_once) {
   const long long N = static_cast<long long>(p.B) * p.L;
   const int rows = kRopeThreads / (p.d > 256 ? p.d / 16 : p.d / 8);
-  const int most = std::min(RT, rows);
+  const int most = p.d > 256 ? 4 : std::min(kRopeMaxTokens, rows);  // d = 512: the angles' table stays at 8 KB
+  // A padded batch's tiles are unequal, some without a token: its blocks get at least four tiles
+  // each, apart from one another (prompts of 1 .. 2048 tokens padded to 8 x 2048, 48 heads x 128: TIMES
+  // us on GB300 against 67.4 in runs).
+  p.scattered = append && p.counts && N >= 4LL * 4 * blocks;
   p.tokens = 1;
-  while (2 * p.tokens <= most && (2LL * p.tokens * blocks <= N || (p.tokens < TMIN && p.tokens < N))) p.tokens *= 2;
+  while (2 * p.tokens <= most && ((p.scattered ? 4 : 1) * 2LL * p.tokens * blocks <= N || (p.tokens < 4 && p.tokens < N))) p.tokens *= 2;
   for (p.at_once = at_once;; p.at_once >>= 1) {
     const int per = rows / p.tokens * p.at_once;
     p.steps_q = (p.Hq + per - 1) / per;
@@ -698,9 +695,8 @@ auto pick_bwd(bool bf, bool inter, int d) {
 
 template <bool APPEND>
 cudaError_t launch_rows(RopeLaunch &a) {
-  const bool norm = a.p.q_w != nullptr || a.p.k_w != nullptr;
-  const int E = a.p.d > 256 ? 16 : 8;
-  const int grid = plan(a.p, APPEND, a.sm_count * rope_resident(E, norm), (E == 16 ? kAtOnce<16> : kAtOnce<8>));
+  const bool norm = a.p.q_w != nullptr || a.p.k_w != nullptr, wide = a.p.d > 256;
+  const int grid = plan(a.p, APPEND, a.sm_count * (wide ? kResident<16> : kResident<8>), wide ? kAtOnce<16> : kAtOnce<8>);
   return launch(pick<APPEND>(a.bf16, norm, a.interleaved, a.p.d), dim3(grid), kRopeThreads, turns_bytes(a.p), a.stream, RopeParams(a.p));
 }
 
@@ -710,12 +706,13 @@ cudaError_t launch_rope(RopeLaunch &a) { return launch_rows<false>(a); }
 cudaError_t launch_append(RopeLaunch &a) { return launch_rows<true>(a); }
 
 cudaError_t launch_rope_bwd(RopeLaunch &a) {
-  const int E = a.p.d > 256 ? 16 : 8, resident = E == 16 ? 1 : LBB;
-  const int grid = plan(a.p, false, std::min(kRopeMaxParts, a.sm_count * resident), (E == 16 ? kBwdAtOnce<16> : kBwdAtOnce<8>));
+  const bool wide = a.p.d > 256;
+  const int blocks = a.sm_count * (wide ? kBwdResident<16> : kBwdResident<8>);
+  const int grid = plan(a.p, false, std::min(kRopeMaxParts, blocks), wide ? kBwdAtOnce<16> : kBwdAtOnce<8>);
   const cudaError_t e =
       launch(pick_bwd(a.bf16, a.interleaved, a.p.d), dim3(grid), kRopeThreads, turns_bytes(a.p), a.stream, RopeParams(a.p));
   if (e != cudaSuccess) return e;
-  return launch(rope_dw_kernel, dim3(a.p.d / 32, a.p.k_w ? 2 : 1), 1024, 0, a.stream, static_cast<const float *>(a.p.parts), grid, a.p.d,
+  return launch(rope_dw_kernel, dim3(a.p.d / 16, a.p.k_w ? 2 : 1), 1024, 0, a.stream, static_cast<const float *>(a.p.parts), grid, a.p.d,
                 a.p.dq_w, a.p.dk_w);
 }
 

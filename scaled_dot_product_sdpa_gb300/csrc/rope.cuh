@@ -18,7 +18,7 @@ constexpr unsigned kDevBadPage = 8;    // a page number outside the cache within
 constexpr unsigned kDevBadLength = 9;  // a length that is negative or beyond the page table
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxTokens = 32;     // tokens a block works on at once
-constexpr int kRopeMaxParts = 640;     // partial weight gradients (blocks) of the backward pass
+constexpr int kRopeMaxParts = 320;     // partial weight gradients (blocks) of the backward pass
 
 struct RopeParams {
   const void *q, *k, *v;             // rows [B, H, L, d] by strides; v: append only
@@ -38,6 +38,7 @@ struct RopeParams {
   int at_once;                       // rows of a unit that each thread works on
   int steps, steps_q, steps_k;       // units of a tile: all, of q, of k (and of v)
   long long units;                   // in all
+  int scattered;                     // blocks take whole tiles, apart from one another
   // append
   void *k_pages, *v_pages;           // [pages, Hkv, page, d] by strides
   long long page_s, head_s, slot_s;
