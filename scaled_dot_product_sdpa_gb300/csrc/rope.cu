@@ -270,39 +270,27 @@ __device__ __forceinline__ void load_turns(const float2 *table, int token, int t
 
 // The units of this block, as a run over tiles and steps; a step is a run of heads of one tensor.
 struct Units {
-  long long tile;
-  int step, stride;  // stride: from tile to tile
-  long long left;
+  int tile, step, left;  // B L fits 31 bits, and so do a block's units (2^40 rows in all at most)
 };
 __device__ __forceinline__ Units units_of(const RopeParams &p) {
-  Units u;
-  if (p.scattered) {  // whole tiles, gridDim.x apart
-    const long long tiles = p.units / p.steps;
-    u.tile = blockIdx.x;
-    u.step = 0;
-    u.stride = gridDim.x;
-    u.left = (tiles - blockIdx.x + gridDim.x - 1) / gridDim.x * p.steps;
-    return u;
-  }
   const long long u0 = p.units * blockIdx.x / gridDim.x, u1 = p.units * (blockIdx.x + 1) / gridDim.x;
-  u.stride = 1;
-  u.tile = u0 / p.steps;
-  u.step = static_cast<int>(u0 - u.tile * p.steps);
-  u.left = u1 - u0;
+  Units u;
+  u.tile = static_cast<int>(u0 / p.steps);
+  u.step = static_cast<int>(u0 - static_cast<long long>(u.tile) * p.steps);
+  u.left = static_cast<int>(u1 - u0);
   return u;
 }
 
 // A thread's token in the current tile.
 struct Token {
-  long long b, l;
+  int b, l;
   bool in;  // whether there is one
 };
-__device__ __forceinline__ Token token_of(const RopeParams &p, long long n) {
+__device__ __forceinline__ Token token_of(const RopeParams &p, int n) {
   Token t;
-  t.in = n < static_cast<long long>(p.B) * p.L;
-  const uint32_t b = t.in ? static_cast<uint32_t>(n) / static_cast<uint32_t>(p.L) : 0;  // B L fits 31 bits
-  t.b = b;
-  t.l = t.in ? n - static_cast<long long>(b) * p.L : 0;
+  t.in = n < p.B * p.L;
+  t.b = t.in ? n / p.L : 0;
+  t.l = t.in ? n - t.b * p.L : 0;
   return t;
 }
 __device__ __forceinline__ const uint16_t *row_at(const void *p, const Token &t, long long batch, long long row) {
@@ -337,7 +325,7 @@ __global__ void __launch_bounds__(kRopeThreads, kResident<E>) rope_kernel(const 
   long long to = 0;
   Turn<E> turn;
   for (; u.left > 0; --u.left) {
-    const long long n0 = u.tile * p.tokens;
+    const int n0 = u.tile * p.tokens;
     if (fresh) {
       tok = token_of(p, n0 + token);
       reads = tok.in;
@@ -373,7 +361,7 @@ __global__ void __launch_bounds__(kRopeThreads, kResident<E>) rope_kernel(const 
         const Token t = token_of(p, n0 + threadIdx.x);
         int x = 0;
         if constexpr (!APPEND) {
-          if (t.in) x = p.positions ? p.positions[t.b * p.pos_s + t.l] : static_cast<int>(t.l);
+          if (t.in) x = p.positions ? p.positions[t.b * p.pos_s + t.l] : t.l;
         } else {
           long long cl = -2;
           if (t.in) {
@@ -381,7 +369,7 @@ __global__ void __launch_bounds__(kRopeThreads, kResident<E>) rope_kernel(const 
             if (count < 0 || count > p.L || len < count || len > static_cast<long long>(p.table_w) * p.page) {
               atomicCAS(p.status, 0u, kDevBadLength);
             } else if (t.l < count) {
-              x = len - count + static_cast<int>(t.l);
+              x = len - count + t.l;
               const int index = x / p.page, page = p.table[t.b * p.table_s + index];
               cl = -1;
               if (page < 0 || page >= p.pages)
@@ -405,7 +393,7 @@ __global__ void __launch_bounds__(kRopeThreads, kResident<E>) rope_kernel(const 
     const bool paged = APPEND && kind != 0;
     const uint32_t dst_h = paged ? static_cast<uint32_t>(p.head_s) : out_h;
     uint16_t *dst = static_cast<uint16_t *>(paged ? (kind == 1 ? p.k_pages : p.v_pages) : kind == 0 ? p.q_out : p.k_out) +
-                    (paged ? max(to, 0LL) : tok.b * heads * static_cast<long long>(out_h) + tok.l * p.d) + static_cast<uint64_t>(h0) * dst_h;
+                    (paged ? max(to, 0LL) : static_cast<long long>(tok.b) * heads * out_h + static_cast<long long>(tok.l) * p.d) + static_cast<uint64_t>(h0) * dst_h;
     const bool copies = APPEND && (plain || kind == 2), clears = APPEND && kind == 0 && to == -2;
     const int stored = APPEND && kind != 0 && to < 0 ? 0 : rows_here;
     const uint64_t step = static_cast<uint64_t>(groups) * dst_h;
@@ -451,7 +439,7 @@ __global__ void __launch_bounds__(kRopeThreads, kResident<E>) rope_kernel(const 
     }
     if (++u.step == p.steps) {
       u.step = 0;
-      u.tile += u.stride;
+      ++u.tile;
       fresh = true;
     }
   }
@@ -501,7 +489,7 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdResident<E>) rope_bwd_kernel
   Token tok;
   Turn<E> turn;
   for (; u.left > 0; --u.left) {
-    const long long n0 = u.tile * p.tokens;
+    const int n0 = u.tile * p.tokens;
     if (fresh) tok = token_of(p, n0 + token);
     const bool is_q = u.step < p.steps_q;
     if (is_q != last_q) add_up(last_q ? 0 : 1);
@@ -534,7 +522,7 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdResident<E>) rope_bwd_kernel
       __syncthreads();
       if (threadIdx.x < p.tokens) {
         const Token t = token_of(p, n0 + threadIdx.x);
-        pos[threadIdx.x] = !t.in ? 0 : p.positions ? p.positions[t.b * p.pos_s + t.l] : static_cast<int>(t.l);
+        pos[threadIdx.x] = !t.in ? 0 : p.positions ? p.positions[t.b * p.pos_s + t.l] : t.l;
       }
       __syncthreads();
       if (p.rotary > 0) {
@@ -543,8 +531,8 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdResident<E>) rope_bwd_kernel
       }
       load_turns<E>(turns, token, p.tokens, at, turn);
     }
-    uint16_t *dst = static_cast<uint16_t *>(is_q ? p.q_out : p.k_out) + tok.b * heads * static_cast<long long>(out_h) +
-                          tok.l * p.d + static_cast<uint64_t>(h0) * out_h;
+    uint16_t *dst = static_cast<uint16_t *>(is_q ? p.q_out : p.k_out) + static_cast<long long>(tok.b) * heads * out_h +
+                    static_cast<long long>(tok.l) * p.d + static_cast<uint64_t>(h0) * out_h;
     Pairs<E> w;
     weight_pairs<E>(weights + (is_q ? 0 : p.d), at.lane, w);
     const uint64_t step = static_cast<uint64_t>(groups) * out_h;
@@ -592,7 +580,7 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdResident<E>) rope_bwd_kernel
     }
     if (++u.step == p.steps) {
       u.step = 0;
-      u.tile += u.stride;
+      ++u.tile;
       fresh = true;
     }
   }
@@ -655,12 +643,8 @@ int plan(RopeParams &p, bool append, int blocks, int at_once) {
   const long long N = static_cast<long long>(p.B) * p.L;
   const int rows = kRopeThreads / (p.d > 256 ? p.d / 16 : p.d / 8);
   const int most = p.d > 256 ? 4 : std::min(kRopeMaxTokens, rows);  // d = 512: the angles' table stays at 8 KB
-  // A padded batch's tiles are unequal, some without a token: its blocks get at least four tiles
-  // each, apart from one another (prompts of 1 .. 2048 tokens padded to 8 x 2048, 48 heads x 128: TIMES
-  // us on GB300 against 67.4 in runs).
-  p.scattered = append && p.counts && N >= 4LL * 4 * blocks;
   p.tokens = 1;
-  while (2 * p.tokens <= most && ((p.scattered ? 4 : 1) * 2LL * p.tokens * blocks <= N || (p.tokens < 4 && p.tokens < N))) p.tokens *= 2;
+  while (2 * p.tokens <= most && (2LL * p.tokens * blocks <= N || (p.tokens < 4 && p.tokens < N))) p.tokens *= 2;
   for (p.at_once = at_once;; p.at_once >>= 1) {
     const int per = rows / p.tokens * p.at_once;
     p.steps_q = (p.Hq + per - 1) / per;

@@ -38,7 +38,6 @@ struct RopeParams {
   int at_once;                       // rows of a unit that each thread works on
   int steps, steps_q, steps_k;       // units of a tile: all, of q, of k (and of v)
   long long units;                   // in all
-  int scattered;                     // blocks take whole tiles, apart from one another
   // append
   void *k_pages, *v_pages;           // [pages, Hkv, page, d] by strides
   long long page_s, head_s, slot_s;
