@@ -9,7 +9,7 @@
 #include <cstdlib>
 
 #include "abi_host.cuh"
-#include "attn_decode_paged.cuh"
+#include "paged_decode.cuh"
 #include "cache_copy.cuh"
 #include "gbattn.h"
 #include "rope.cuh"

@@ -1,4 +1,4 @@
-// attn_decode_paged.cu -- decoding over a paged cache (see attn_decode_paged.cuh).
+// paged_decode.cu -- decoding over a paged cache (see paged_decode.cuh).
 //
 // Bound by the HBM reads of K and V: a key head's rows are used by G query heads, 2 G FLOPs per
 // byte, more than the CUDA cores can do at HBM speed from G = 4 on.  So both products run on
@@ -20,9 +20,9 @@
 // a TMA producer and an MMA issuer.  K and V tiles pass through one ring of 128-key x 128-column
 // slots (64 columns at d = 64) in the order K0 K1 V0 K2 V1 ...; QK runs a tile ahead of PV.
 // Pages of fewer than 128 slots make several TMA boxes per slot, one per producer lane.
-#include "attn_decode_paged.cuh"
+#include "paged_decode.cuh"
 #include "attn_fwd_kernel.cuh"
-#include "ptx.cuh"
+#include "ptx_paged.cuh"
 #include "rope.cuh"
 #include "vec16.cuh"
 

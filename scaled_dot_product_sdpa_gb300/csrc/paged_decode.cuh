@@ -1,4 +1,4 @@
-// attn_decode_paged.cuh -- attention of one new token per sequence over a paged key/value
+// paged_decode.cuh -- attention of one new token per sequence over a paged key/value
 // cache: parameters and launch entry point.
 //
 // For sequence b with n = lengths[b] cached tokens and query head h, which shares the keys

@@ -27,7 +27,7 @@
 // of 10^6 costs no accuracy, where an fp32 product would be off by 0.06 radians).
 #include <algorithm>
 
-#include "ptx.cuh"
+#include "ptx_paged.cuh"
 #include "rope.cuh"
 #include "vec16.cuh"
 

@@ -1,4 +1,4 @@
-"""Host models of the paged decode kernel's bookkeeping (csrc/attn_decode_paged.cu), which need no GPU: the shares of the CTAs cover
+"""Host models of the paged decode kernel's bookkeeping (csrc/paged_decode.cu), which need no GPU: the shares of the CTAs cover
 every tile once and name the partial results that belong together, and the ring's protocol never stalls and never lets a slot be
 refilled or a buffer rewritten too early."""
 import random
