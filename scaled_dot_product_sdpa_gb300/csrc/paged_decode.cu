@@ -226,30 +226,34 @@ struct Walk {
 struct Cursor {
   Walk<false> w;
   Seg s;
-  int i = 0, seg = -1, row, index = 0, slot = 0;  // index: in the sequence's table row
+  int i = 0, seg = -1, row;
+  int index = 0, slot = 0;   // index: in the sequence's table row
+  int keys = 0, behind = 0;  // valid keys in the tile; tokens of the sequence from the tile's first on
+  int head = 0;
   __device__ Cursor(const PagedParams &p, const Start &at, int r) : w(p, at), row(r) { s.count = 0; }
   __device__ bool next() {
-    const int page = w.p.page;
     if (i == s.count) {
       if (!w.next(s)) return false;
       i = 0;
       ++seg;
-      const int pos = s.tile * kPagedTile + row;
-      index = pos / page;
-      slot = pos - index * page;
+      const int first = s.tile * kPagedTile, pos = first + row;
+      index = pos / w.p.page;
+      slot = pos - index * w.p.page;
+      behind = s.len - first;
+      head = w.p.blocks == 1 ? s.hv : s.hv / w.p.blocks;
     } else {
       index += w.p.tile_pages;
       slot += w.p.tile_slots;
-      if (slot >= page) {
-        slot -= page;
+      if (slot >= w.p.page) {
+        slot -= w.p.page;
         ++index;
       }
+      behind -= kPagedTile;
     }
     ++i;
+    keys = min(kPagedTile, behind);
     return true;
   }
-  // valid keys in the tile
-  __device__ int keys() const { return min(kPagedTile, s.len - (s.tile + i - 1) * kPagedTile); }
   __device__ bool first() const { return i == 1; }
 };
 
@@ -363,8 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 5) {
     // ---------------------------------------------------------- producers
     const int which = warp - 5;
-    // Every lane runs on its own: it waits for a slot and copies its box, if it has one in the tile
-    // (boxes of K and V are dealt out over the producers); lane 0 also announces the producer's bytes.
+    // A lane copies its box of a slot, if it has one in the tile (boxes of K and V are dealt out over
+    // the producers); lane 0 waits for the slot and announces the producer's bytes.
     const int rows = p.box_rows, lanes = kPagedTile / rows * C::NBOX;
     const int row = (lane / C::NBOX) * rows, box = lane % C::NBOX;  // this lane's box of a slot
     const bool deals_k = lane < lanes && lane % kProducers == which;
@@ -378,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Cursor pre(p, start, row), it(p, start, row);
     uint32_t stage = 0;
     auto prefetch = [&]() {
-      if (deals && pre.next() && row < pre.keys()) cp_async_4(mine_p + stage * 128, p.table + pre.s.b * p.table_s + pre.index);
+      if (deals && pre.next() && row < pre.keys) cp_async_4(mine_p + stage * 128, p.table + pre.s.b * p.table_s + pre.index);
       cp_async_commit();
       stage = stage + 1 == kAhead ? 0 : stage + 1;
     };
@@ -389,8 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto look = [&](Load &l) -> bool {  // the next tile, and this lane's page of it
       if (!it.next()) return false;
-      l.keys = it.keys();
-      l.head = it.s.hv / p.blocks;
+      l.keys = it.keys;
+      l.head = it.head;
       l.slot = it.slot;
       l.page = 0;
       cp_async_wait<kAhead - 1>();
@@ -401,18 +405,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       prefetch();
       return true;
     };
-    auto fill = [&](const Load &l, const CUtensorMap *tm, bool deal, int first) {
-      // boxes of this producer in the tile: lanes first, first + kProducers, ... below the used ones
-      const int used = (l.keys + rows - 1) / rows * C::NBOX;
-      const uint32_t bytes = used > first ? static_cast<uint32_t>((used - first + kProducers - 1) / kProducers * rows) * 128u : 0u;
-      for (int c = 0; ok && c < C::NC; ++c) {
-        if (filled == C::NSLOT)
+    // Bytes of this producer in a tile of `keys`: boxes first, first + kProducers, ... of the used ones.
+    const int shift = 31 - __clz(rows);
+    auto bytes_of = [&](int keys, int first) -> uint32_t {
+      const int used = ((keys + rows - 1) >> shift) * C::NBOX;
+      return used > first ? static_cast<uint32_t>((used - first + kProducers - 1) / kProducers * rows) * 128u : 0u;
+    };
+    const int first_k = which, first_v = (which + kProducers - lanes % kProducers) % kProducers;
+    const uint32_t full_k = bytes_of(kPagedTile, first_k), full_v = bytes_of(kPagedTile, first_v);
+    auto fill = [&](const Load &l, const CUtensorMap *tm, bool deal, int first, uint32_t full) {
+      const uint32_t bytes = l.keys == kPagedTile ? full : bytes_of(l.keys, first);
+      deal = deal && row < l.keys;
+      for (int c = 0; c < C::NC; ++c) {
+        // The first lap passes at once: the phase before a barrier's first counts as complete.  Lane 0
+        // waits for all: a lane that tested the barrier by itself could come so late that the slot
+        // had been filled and freed once more, and its parity would not come round again.
+        if (lane == 0)
           ok = wait_bounded(BAR(C::B_EMPTY + slot), lap ^ 1u, &misc.abort_flag, p.status, kDevTimeoutLoad, p.wait_limit);
-        else
-          ++filled;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
+        if (filled < C::NSLOT) ++filled;
         if (lane == 0) mbar_arrive_expect_tx(BAR(C::B_FULL + slot), bytes);
-        if (deal && row < l.keys)
+        if (deal)
           tma_load_4d(base + slot * C::SLOT_BYTES + box * C::BOX_BYTES + row * 128, tm, c * C::CW + box * 64, l.slot, l.head, l.page,
                       BAR(C::B_FULL + slot));
         if (++slot == C::NSLOT) {
@@ -421,7 +435,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     };
-    const int first_k = which, first_v = (which + kProducers - lanes % kProducers) % kProducers;
     auto query = [&]() {  // Q of a segment, before its first K
       const int s = it.seg;
       if (s >= C::NQB) ok = wait_bounded(BAR(C::B_QEMPTY + s % C::NQB), (s / C::NQB - 1) & 1, &misc.abort_flag, p.status, kDevTimeoutLoad, p.wait_limit);
@@ -429,17 +442,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       queries = s + 1;
       const uint32_t bar = BAR(C::B_QFULL + s % C::NQB), dst = base + C::OFF_Q + (s % C::NQB) * C::Q_BYTES;
       mbar_arrive_expect_tx(bar, static_cast<uint32_t>(p.q_rows) * 128u * (D / 64));
-      const int head = (it.s.hv / p.blocks) * p.G + (it.s.hv % p.blocks) * NH;
+      const int head = it.head * p.G + (it.s.hv - it.head * p.blocks) * NH;
       for (int x = 0; x < D / 64; ++x) tma_load_3d(dst + x * C::NQ * 128, &tm_q, x * 64, head, it.s.b, bar);
     };
     Load v, k;
     bool have_v = false, have_k = look(k);
     while (ok && (have_k || have_v)) {
       if (have_k) {
-        if (which == kProducers - 1 && lane == 0 && it.first()) query();
-        if (ok) fill(k, &tm_k, deals_k, first_k);
+        if (it.first()) {
+          if (which == kProducers - 1 && lane == 0) query();
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        if (ok) fill(k, &tm_k, deals_k, first_k, full_k);
       }
-      if (ok && have_v) fill(v, &tm_v, deals_v, first_v);
+      if (ok && have_v) fill(v, &tm_v, deals_v, first_v, full_v);
       v = k;
       have_v = have_k;
       have_k = have_k && look(k);
