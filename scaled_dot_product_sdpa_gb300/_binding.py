@@ -518,7 +518,7 @@ def attn_rope(q, k, inv_freq, positions=None, interleaved: bool = False, factor:
     wq, wk = _norm_weights(q_weight, k_weight, d, dev, dtype, True, k is not None)
     q_out = _empty(shape, dtype, q, stream) if q_out is None else _check_out(q_out, "q_out", shape, dtype, dev)
     _launch("attn_rope", (_lib or load_library()).attn_rope, dev, stream, *_rows(q, "q", shape), *kr, q_out.data_ptr(), k_to,
-            fp, rotary, bool(interleaved), factor, pp, ps, wq, wk, eps, code, B, Hq, Hkv, L, d)
+            fp, rotary, bool(interleaved), float(factor), pp, ps, wq, wk, float(eps), code, B, Hq, Hkv, L, d)
     return q_out, k_out
 
 
@@ -572,7 +572,7 @@ def attn_rope_bwd(dq, dk, inv_freq, positions=None, interleaved: bool = False, f
         ws = workspace.data_ptr()
     dq_out = _empty(shape, dtype, dq, stream) if dq_out is None else _check_out(dq_out, "dq_out", shape, dtype, dev)
     _launch("attn_rope_bwd", lib.attn_rope_bwd, dev, stream, *_rows(dq, "dq", shape), *kr, *xq, *xk, dq_out.data_ptr(), k_to,
-            wq_to, wk_to, fp, rotary, bool(interleaved), factor, pp, ps, wq, wk, eps, ws, code, B, Hq, Hkv, L, d)
+            wq_to, wk_to, fp, rotary, bool(interleaved), float(factor), pp, ps, wq, wk, float(eps), ws, code, B, Hq, Hkv, L, d)
     if wq is None:
         return dq_out, dk_out
     return dq_out, dk_out, dq_weight, (dk_weight if dk is not None else None)
@@ -636,7 +636,7 @@ def attn_cache_append(k, v, k_pages, v_pages, table, lengths, counts=None, q=Non
     fp, rotary = _frequencies(inv_freq, dev)
     wq, wk = _norm_weights(q_weight, k_weight, d, dev, dtype, q is not None, True)
     _launch("attn_cache_append", (_lib or load_library()).attn_cache_append, dev, stream, *_rows(k, "k", shape),
-            *_rows(v, "v", shape), *qr, q_to, *cache, tp, ts, tw, lp, cp, fp, rotary, bool(interleaved), factor, wq, wk, eps,
+            *_rows(v, "v", shape), *qr, q_to, *cache, tp, ts, tw, lp, cp, fp, rotary, bool(interleaved), float(factor), wq, wk, float(eps),
             code, B, Hq, Hkv, L, d)
     return q_out if q is not None else None
 
@@ -696,5 +696,5 @@ def attn_decode_paged(q, k_pages, v_pages, table, lengths, scale: float | None =
     workspace = _workspace(workspace, nbytes, q, dev, stream)
     _launch("attn_decode_paged", lib.attn_decode_paged, dev, stream, q.data_ptr(), strides[0] if B > 1 else 0,
             strides[1] if Hq > 1 else 0, *cache, tp, ts, tw, lp, o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), code, B, Hq,
-            Hkv, d, 1.0 / math.sqrt(d) if scale is None else scale)
+            Hkv, d, 1.0 / math.sqrt(d) if scale is None else float(scale))
     return o, lse

@@ -200,7 +200,7 @@ struct Walk {
     }
   }
   __device__ bool next(Seg &s) {
-    if (left <= 0) return false;
+    if (left <= 0 || b >= p.B) return false;  // (b ends in time unless the lengths change under the kernel)
     s.b = b;
     s.hv = hv;
     s.len = length();
@@ -345,16 +345,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long u0 = total * cta / G, u1 = total * min(cta + 1, G) / G;
   if (u0 < u1 && upto - mine <= u0 && u0 < upto) {
     long long off = u0 - (upto - mine);
-    int b = s0, n = len0;
-    for (;; n = clamp_length(p.lengths[++b], p)) {  // ends before s1: the run holds unit u0
+    int n = len0;
+    for (int b = s0; b < s1; ++b) {
+      if (b > s0) n = clamp_length(p.lengths[b], p);
       const long long units = static_cast<long long>(tiles_of(n)) * hvs;
-      if (off < units) break;
-      off -= units;
+      if (off >= units) {
+        off -= units;
+        continue;
+      }
+      const unsigned long long nt = static_cast<unsigned long long>(tiles_of(n)), o = static_cast<unsigned long long>(off);
+      // 32-bit division where it serves (it nearly always does)
+      const unsigned long long hv = (o >> 32) == 0 ? static_cast<uint32_t>(o) / static_cast<uint32_t>(nt) : o / nt;
+      misc.start = {b, n, static_cast<int>(hv), static_cast<int>(o - hv * nt), u1 - u0};
+      break;
     }
-    const unsigned long long nt = static_cast<unsigned long long>(tiles_of(n)), o = static_cast<unsigned long long>(off);
-    // 32-bit division where it serves (it nearly always does)
-    const unsigned long long hv = (o >> 32) == 0 ? static_cast<uint32_t>(o) / static_cast<uint32_t>(nt) : o / nt;
-    misc.start = {b, n, static_cast<int>(hv), static_cast<int>(o - hv * nt), u1 - u0};
   }
   tc_fence_before();
   __syncthreads();
@@ -596,14 +600,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t from = lanes + C::T_O + (due.seg & 1) * (C::NO * C::NP);
       float inv[NH];
 #pragma unroll
-      for (int g = 0; g < NH; g += 4)
+      for (int g = 0; g < NH; g += 4) {
+        inv[g] = inv[g + 1] = inv[g + 2] = inv[g + 3] = 0.f;
         if (g < due.heads) {
           const float4 *const r = reinterpret_cast<const float4 *>(sums + g);
           const float4 a = r[0], b = r[NH / 4], c = r[2 * NH / 4], d = r[3 * NH / 4];
           const float t[4] = {(a.x + b.x) + (c.x + d.x), (a.y + b.y) + (c.y + d.y), (a.z + b.z) + (c.z + d.z), (a.w + b.w) + (c.w + d.w)};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) inv[g + e] = t[e] == 0.f ? 0.f : 1.f / t[e];
+          for (int e = 0; e < 4; ++e) inv[g + e] = t[e] == 0.f ? 0.f : __fdividef(1.f, t[e]);  // t < 2^126: 2 ulp
         }
+      }
       if (ok && tid < due.heads) {
         const float lse2 = tops[tid] - kShift + __log2f((sums[tid] + sums[NH + tid]) + (sums[2 * NH + tid] + sums[3 * NH + tid]));
         if (due.whole)
@@ -616,18 +622,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t o[C::NP];
         tmem_ld<C::NP>(from + ob * C::NP, o);
         const int col = ob * 128 + tid;
-        if (ok && (D >= 128 || tid < D))
+        if (!ok || (D < 128 && tid >= D)) continue;
 #pragma unroll
-          for (int h = 0; h < NH; ++h)
-            if (h < due.heads) {
-              const float y = (__uint_as_float(o[h]) + __uint_as_float(o[NH + h])) * inv[h];
-              if (!due.whole)
-                p.part_o[(part * NH + h) * D + col] = y;
-              else if (p.bf16)
-                static_cast<__nv_bfloat16 *>(p.o)[(due.row0 + h) * D + col] = __float2bfloat16_rn(y);
-              else
-                static_cast<__half *>(p.o)[(due.row0 + h) * D + col] = __float2half_rn(y);
-            }
+        for (int h = 0; h < NH; ++h) o[h] = __float_as_uint((__uint_as_float(o[h]) + __uint_as_float(o[NH + h])) * inv[h]);
+        if (!due.whole) {
+          float *to = p.part_o + part * NH * D + col;
+#pragma unroll
+          for (int h = 0; h < NH; ++h, to += D)
+            if (h < due.heads) *to = __uint_as_float(o[h]);
+        } else {
+          uint16_t *to = static_cast<uint16_t *>(p.o) + due.row0 * D + col;
+#pragma unroll
+          for (int h = 0; h < NH; h += 2, to += 2 * D) {
+            const uint32_t two = p.bf16 ? pack2<true>(__uint_as_float(o[h]), __uint_as_float(o[h + 1]))
+                                        : pack2<false>(__uint_as_float(o[h]), __uint_as_float(o[h + 1]));
+            if (h < due.heads) to[0] = static_cast<uint16_t>(two);
+            if (h + 1 < due.heads) to[D] = static_cast<uint16_t>(two >> 16);
+          }
+        }
       }
       tc_fence_before();
       due.heads = 0;

@@ -111,6 +111,35 @@ def test_append(B, Hq, Hkv, L, d, page, layout, dtype, mode):
     assert (out.cpu()[~mask.expand_as(qw)] == 0).all()
 
 
+@pytest.mark.parametrize("d", [64, 128, 256, 512])
+@pytest.mark.parametrize("weights", [False, True])
+def test_append_without_rotation(d, weights):
+    """Queries beside keys with nothing to compute are copied (zeros behind counts); with weights alone both are normalised."""
+    B, Hq, Hkv, L, page = 3, 6, 2, 20, 8
+    counts = torch.tensor([20, 0, 7], dtype=torch.int32)
+    lengths = counts + 3
+    store, view = cache("heads", 12, Hkv, page, d, torch.float16, 71)
+    table = tables(lengths.tolist(), page, 12, 72)
+    q, k, v = (draw((B, L, H, d), torch.float16, 73 + H).transpose(1, 2) for H in (Hq, Hkv, Hkv))
+    wq, wk = (draw((d,), torch.float16, 74 + n).cuda() if weights else None for n in (0, 1))
+    there = store.cuda()
+    out = gb.attn_cache_append(k.cuda(), v.cuda(), *view(there), table.cuda(), lengths.cuda(), counts=counts.cuda(), q=q.cuda(), q_weight=wq, k_weight=wk)
+    kg, vg = view(there.cpu())
+
+    def normed(x, w):
+        y = x.double()
+        return y if w is None else y / (y.square().mean(-1, keepdim=True) + 1e-6).sqrt() * w.cpu().double()
+
+    qn, kn = normed(q, wq), normed(k, wk)
+    for b, c in enumerate(counts.tolist()):
+        check(out[b, :, :c], qn[b, :, :c], qn[b, :, :c].abs() * weights, "queries")
+        assert (out[b, :, c:] == 0).all()
+        for t in range(c):
+            at = int(table[b, (3 + t) // page]), slice(None), (3 + t) % page
+            check(kg[at], kn[b, :, t], kn[b, :, t].abs() * weights, "keys")
+            assert torch.equal(vg[at], v[b, :, t])
+
+
 def test_append_leaves_bad_sequences_out():
     """A length beyond the table, a count above L or above the length, a negative count: the sequence is left out; a page outside the
     cache: the token is.  All others are written, and the status word says what was found first."""
@@ -269,6 +298,19 @@ def test_decode_peaks_and_tails(dtype):
     check_decode(gb.attn_decode_paged(q.cuda(), kp.cuda(), vp.cuda(), table.cuda(), n.cuda(), scale=1.0), decode_reference(q, kp, vp, table, n, 1.0))
 
 
+def test_decode_of_repeated_inputs():
+    """One query row for all heads and sequences, one table row and one page for all: strides of 0."""
+    H, d, page, B = 2, 128, 16, 3
+    store, view = cache("heads", 2, H, page, d, torch.bfloat16, 75)
+    kp, vp = view(store)
+    q = draw((1, 1, d), torch.bfloat16, 76).expand(B, 4, d)
+    table, n = torch.tensor([[1, 0]], dtype=torch.int32).expand(B, 2), torch.tensor([30, 5, 17], dtype=torch.int32)
+    wide = q[:1, :1].cuda().expand(B, 4, d)
+    assert wide.stride()[:2] == (0, 0)
+    got = gb.attn_decode_paged(wide, kp.cuda(), vp.cuda(), table[:1].cuda().expand(B, 2), n.cuda())
+    check_decode(got, decode_reference(q, kp, vp, table, n, 1.0 / math.sqrt(d)))
+
+
 def test_decode_bad_pages_and_lengths():
     """A page outside the cache counts as zeros, a negative length as none, one beyond the table as its end; the status word tells,
     other sequences are not affected."""
@@ -285,6 +327,22 @@ def test_decode_bad_pages_and_lengths():
     check_decode(got, ref)
     check_decode(gb.attn_decode_paged(q[:1].cuda(), kp.cuda(), vp.cuda(), table[:1].cuda(), torch.tensor([32], dtype=torch.int32).cuda(), scale=0.1),
                  [x[:1] for x in ref])
+
+
+@pytest.mark.parametrize("d,page,Hkv,G", [(512, 16, 2, 1), (512, 128, 1, 8), (256, 8, 1, 20), (64, 8, 3, 2), (128, 24, 2, 16)])
+def test_decode_many_times(d, page, Hkv, G):
+    """The kernel's warps meet in many orders: a few thousand calls give the same bits, and no wait runs out."""
+    lengths = [1000, 3, 0, 517, 128, 2000]
+    P = sum(-(-m // page) for m in lengths)
+    store, view = cache("heads", P, Hkv, page, d, torch.bfloat16, 77)
+    there, table, n = view(store.cuda()), tables(lengths, page, P, 78).cuda(), torch.tensor(lengths, dtype=torch.int32).cuda()
+    q = draw((len(lengths), Hkv * G, d), torch.bfloat16, 79).cuda()
+    o, lse = gb.attn_decode_paged(q, *there, table, n)
+    differ = torch.zeros((), dtype=torch.int32, device="cuda")
+    for _ in range(3000):
+        a, b = gb.attn_decode_paged(q, *there, table, n)
+        differ += (a != o).any() | (b != lse).any()
+    assert int(differ) == 0
 
 
 def test_decode_agrees_with_the_contiguous_cache():
