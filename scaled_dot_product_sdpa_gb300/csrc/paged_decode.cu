@@ -16,10 +16,18 @@
 // and last rows may be parts of longer ones: those partial results go to the workspace, and
 // paged_merge_kernel joins them in a fixed order (M = max lse, o = sum 2^(lse - M) o / sum).
 //
-// A CTA is six warps: four of softmax (warp w reads TMEM lanes 32 w ..: keys, or columns of O),
-// a TMA producer and an MMA issuer.  K and V tiles pass through one ring of 128-key x 128-column
-// slots (64 columns at d = 64) in the order K0 K1 V0 K2 V1 ...; QK runs a tile ahead of PV.
-// Pages of fewer than 128 slots make several TMA boxes per slot, one per producer lane.
+// A CTA is eight warps: four of softmax (warp w reads TMEM lanes 32 w ..: keys, or columns of O),
+// an MMA issuer (one thread) and three TMA producers.  K and V tiles pass through one ring of
+// slots (128 keys x 64 or 128 columns) in the order K0 K1 V0 K2 V1 ...; QK runs a tile ahead of PV,
+// and a row's results are taken after the next row's first tile.  Pages of fewer than 128 slots
+// make several TMA boxes per slot; a producer issues one in about 53 cycles, so the boxes are dealt
+// over three of them (one: pages of 8 tokens 645 us, of 16 454, of 128 302; three: 305, 301, 298).
+//
+// Measured on GB300 (64 sequences x 8 key heads x 8000 tokens, d = 128, bf16; 2.1 GB): 298 to 307 us for
+// pages of 8 to 128 tokens and up to 8 query heads to a key head, 6.8 to 7.0 TB/s (103% of the copy
+// bandwidth: a read-only stream); 16 query heads 307 to 321; d = 64 309 to 315; d = 256 298 to 302; d = 512
+// 316 to 319.  One sequence of 1000 tokens: 9.2 us, the chain of launch, lengths, table, load, two
+// products and the join.
 #include "paged_decode.cuh"
 #include "attn_fwd_kernel.cuh"
 #include "ptx_paged.cuh"
@@ -37,28 +45,32 @@ constexpr float kSlack = 2.f;   // the running maximum moves when a logit exceed
 
 template <int D, int NH>
 struct PagedCfg {
-  static constexpr int CW = D == 64 ? 64 : 128;         // columns of a ring slot
+  static constexpr int RES = paged_resident(D, NH);      // CTAs on an SM
+  static constexpr int CW = D == 64 || RES == 2 ? 64 : 128;  // columns of a ring slot
   static constexpr int NC = D / CW;                     // slots of a K or V tile
   static constexpr int NBOX = CW / 64;                  // 64-column boxes of a slot
   static constexpr int BOX_BYTES = kPagedTile * 128;
   static constexpr int SLOT_BYTES = NBOX * BOX_BYTES;
+  static constexpr int VS = D >= 128 && CW == 64 ? 2 : 1;  // slots of a PV product (128 columns of V)
   static constexpr int NQ = NH < 16 ? 16 : NH;          // rows of the Q operand (a product of 128 rows has N % 16 = 0)
-  static constexpr int Q_BYTES = NQ * D * 2;
+  static constexpr int Q_BYTES = NH * D * 2;            // the operand's rows from NH on are whatever follows: their columns of S are not read
   static constexpr int NP = 2 * NH;                     // columns of P^T: hi parts, then lo parts
   static constexpr int P_BYTES = NP * kPagedTile * 2;
-  static constexpr int NQB = NH == 8 && D <= 128 ? 4 : NH == 32 && D == 256 ? 1 : 2;  // query buffers: segments looked ahead
+  static constexpr int NQB = NH == 8 && D <= 128 && RES == 1 ? 4 : NH == 32 && D == 256 ? 1 : 2;  // query buffers: segments looked ahead
   // floats: warps' maxima of two tiles, their sums of two segments, the maxima of two segments
   static constexpr int RED_SUMS = 8 * NH, RED_TOPS = 16 * NH, RED_BYTES = 18 * NH * 4;
   static constexpr int PAGE_BYTES = kProducers * kAhead * 32 * 4;  // page numbers read ahead, per producer lane
   static constexpr int BAR_BYTES = 512;                 // barriers and a few words
-  static constexpr int ROOM = 232448 - 1024 - NQB * Q_BYTES - 2 * P_BYTES - RED_BYTES - PAGE_BYTES - BAR_BYTES;
+  static constexpr int SMEM_MOST = RES == 2 ? 115712 : 232448;  // 228 KB an SM, 1 KB a CTA kept by the system
+  static constexpr int ROOM = SMEM_MOST - 1024 - NQB * Q_BYTES - 2 * P_BYTES - RED_BYTES - PAGE_BYTES - BAR_BYTES;
   static constexpr int FIT = ROOM / SLOT_BYTES, MOST = 196608 / SLOT_BYTES;
-  static constexpr int NSLOT = FIT < MOST ? FIT : MOST;
+  static constexpr int NSLOT = (FIT < MOST ? FIT : MOST) / VS * VS;  // a PV product's slots lie side by side
   // With one slot a tile, the commit that frees K's slot also tells that S is there, and the one that
   // frees V's that PV is done (a commit costs its thread about 190 cycles); nothing else is
   // committed to that slot before the softmax has looked, as the ring holds more than four tiles' slots.
   static constexpr bool ONE = NC == 1;
   static_assert(!ONE || NSLOT >= 5, "slots that the softmax waits on");
+  static_assert(NC % VS == 0, "PV products of whole slots");
   static_assert(NSLOT > NC, "a tile's V slots are resident together while the next K slots pass");
   static constexpr int OFF_Q = NSLOT * SLOT_BYTES;
   static constexpr int OFF_P = OFF_Q + NQB * Q_BYTES;
@@ -69,7 +81,7 @@ struct PagedCfg {
   static constexpr int B_FULL = 0, B_EMPTY = NSLOT, B_QFULL = 2 * NSLOT, B_QEMPTY = B_QFULL + NQB, B_SFULL = B_QEMPTY + NQB,
                        B_PFULL = B_SFULL + 2, B_PDONE = B_PFULL + 2, B_DRAIN = B_PDONE + 2, NBAR = B_DRAIN + 1;
   static constexpr int SMEM_BYTES = 1024 + OFF_BAR + BAR_BYTES;
-  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+  static_assert(SMEM_BYTES <= SMEM_MOST, "shared memory budget");
   static constexpr int NO = D <= 128 ? 1 : D / 128;     // 128-column blocks of O
   static constexpr int T_O = 2 * NQ;                    // TMEM columns: S twice, then O twice
   static constexpr int T_USED = T_O + 2 * NO * NP;       // O of two segments
@@ -262,7 +274,7 @@ __device__ __forceinline__ uint32_t k_pos(uint32_t t, int nc) { return t == 0 ? 
 __device__ __forceinline__ uint32_t v_pos(uint32_t t, uint32_t T, int nc) { return (min(t + 2, T) + t) * nc; }
 
 template <int D, int NH>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, PagedCfg<D, NH>::RES)
     decode_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
   using C = PagedCfg<D, NH>;
@@ -447,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t bar = BAR(C::B_QFULL + s % C::NQB), dst = base + C::OFF_Q + (s % C::NQB) * C::Q_BYTES;
       mbar_arrive_expect_tx(bar, static_cast<uint32_t>(p.q_rows) * 128u * (D / 64));
       const int head = it.head * p.G + (it.s.hv - it.head * p.blocks) * NH;
-      for (int x = 0; x < D / 64; ++x) tma_load_3d(dst + x * C::NQ * 128, &tm_q, x * 64, head, it.s.b, bar);
+      for (int x = 0; x < D / 64; ++x) tma_load_3d(dst + x * NH * 128, &tm_q, x * 64, head, it.s.b, bar);
     };
     Load v, k;
     bool have_v = false, have_k = look(k);
@@ -480,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t idesc_o = p.bf16 ? idesc_bf16_f32(128, C::NP, 1, 1) : idesc_f16_f32(128, C::NP, 1, 1);
     const SDesc dk = sdesc_split(sdesc_sw128(base, 16, 1024));
     // V^T: 64-column boxes BOX_BYTES apart; at d = 64 there is one, read twice (rows 64 .. of O are not used)
-    const SDesc dv = sdesc_split(sdesc_sw128(base, C::NBOX == 1 ? 0 : C::BOX_BYTES, 1024));
+    const SDesc dv = sdesc_split(sdesc_sw128(base, D == 64 ? 0 : C::BOX_BYTES, 1024));
     const SDesc dq = sdesc_split(sdesc_sw128(base + C::OFF_Q, 16, 1024));
     const SDesc dp = sdesc_split(p_desc<NH>(base + C::OFF_P));
     if (lane == 0) {
@@ -508,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < C::CW / 16; ++kk)
               umma_ss_off(tmem + buf * C::NQ, dk, slot * C::SLOT_BYTES + (kk >> 2) * C::BOX_BYTES + (kk & 3) * 32, dq,
-                          qb * C::Q_BYTES + (c * C::NBOX + (kk >> 2)) * C::NQ * 128 + (kk & 3) * 32, idesc_s, (c | kk) != 0);
+                          qb * C::Q_BYTES + (c * C::NBOX + (kk >> 2)) * NH * 128 + (kk & 3) * 32, idesc_s, (c | kk) != 0);
             umma_commit(BAR(C::B_EMPTY + slot));
           }
         }
@@ -520,8 +532,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto pv = [&](uint32_t i, uint32_t seg, bool first) {
         const uint32_t buf = i & 1u, o = tmem + C::T_O + (seg & 1u) * (C::NO * C::NP);
         wait(C::B_PFULL + buf, i >> 1);
-        for (int c = 0; c < C::NC; ++c, step()) {
+        for (int c = 0; c < C::NC / C::VS; ++c) {
           wait(C::B_FULL + slot, lap);
+          if (C::VS == 2) wait(C::B_FULL + slot + 1, lap);
           if (got) {
             tc_fence_after();
 #pragma unroll
@@ -529,7 +542,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               umma_ss_off(o + c * C::NP, dv, slot * C::SLOT_BYTES + kk * 2048, dp, buf * C::P_BYTES + kk * (16 * 4 * NH), idesc_o,
                           !first || kk > 0);
             umma_commit(BAR(C::B_EMPTY + slot));
+            if (C::VS == 2) umma_commit(BAR(C::B_EMPTY + slot + 1));
           }
+          step();
+          if (C::VS == 2) step();
         }
         if (!C::ONE && got) umma_commit(BAR(C::B_PDONE + buf));
       };
@@ -877,7 +893,7 @@ cudaError_t launch_paged(const PagedLaunch &a) {
   // At most one CTA per unit of work that the tables have room for.
   const long long row_tiles = (static_cast<long long>(a.p.table_w) * a.p.page + kPagedTile - 1) / kPagedTile;
   const long long units = static_cast<long long>(a.p.B) * a.p.Hkv * a.p.blocks * row_tiles;
-  const unsigned grid = static_cast<unsigned>(std::min<long long>(units, std::min(a.sm_count, kPagedMaxCtas)));
+  const unsigned grid = static_cast<unsigned>(std::min<long long>(units, std::min(C::RES * a.sm_count, kPagedMaxCtas)));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);

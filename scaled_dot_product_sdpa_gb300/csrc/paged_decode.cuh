@@ -14,7 +14,12 @@
 
 namespace gbattn {
 
-constexpr int kPagedMaxCtas = 152;  // persistent CTAs at most (one per SM); sizes the workspace
+// Persistent CTAs on an SM.  Two where registers and shared memory hold them (up to 8 heads at once,
+// d <= 128): one CTA's tile is a chain of a softmax and two products, and at d = 64 or with short
+// sequences the second fills its gaps (GB300, 128 x 8 heads x 8000 keys x 64 363 us with one, 313 with
+// two; 256 sequences of 100 tokens, 32/8 heads x 128, 38.2 and 31.4; d = 128 long rows the same).
+constexpr int paged_resident(int d, int heads) { return heads == 8 && d <= 128 ? 2 : 1; }
+constexpr int kPagedMaxCtas = 304;  // CTAs at most (two on each SM); sizes the workspace
 constexpr int kPagedTile = 128;     // keys per tile
 
 // Query heads of one key head that a CTA works on at once, and how many such blocks of heads
