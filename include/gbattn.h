@@ -270,9 +270,9 @@ int attn_debug_decode_plan(int B, int H, int L, int d, int sm_count, int max_ran
  *   - Values are fp16 or bf16 (`dtype`), the same for every tensor of a call.
  *   - Rows (queries, keys, values, upstream gradients) are given by a pointer and three
  *     element strides: element (b, h, l, i) lies at b * sb + h * sh + l * sl + i.  Strides are
- *     non-negative multiples of 8, a head's (and L * d) below 2^32; inputs may repeat elements
- *     (stride 0).  So a projection's
- *     output [B, L, Hq + 2 Hkv, d] is read where it lies.  Outputs are contiguous.
+ *     non-negative multiples of 8, a head's (and L * d) below 2^32, and reach at most 2^40
+ *     elements; inputs may repeat elements (stride 0).  So a projection's output
+ *     [B, L, Hq + 2 Hkv, d] is read where it lies.  Outputs are contiguous.
  *   - A cache is two arrays of `pages` pages, for keys and for values, each page holding
  *     `page` slots (a multiple of 8) of Hkv heads: element (page, head, slot, i) lies at
  *     page * sp + head * sh + slot * ss + i in both.  Strides are multiples of 8; the page's

@@ -29,8 +29,12 @@ struct Span {  // bytes [p, p + n)
 
 bool finite_nonneg(float x) { return std::isfinite(x) && x >= 0.f; }
 bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256 || d == 512; }
-bool stride_ok(long long s) { return s >= 0 && s % 8 == 0 && s < (1LL << 39); }
-bool rows_ok(const Rows &r) { return stride_ok(r.sb) && stride_ok(r.sh) && r.sh < (1LL << 32) && stride_ok(r.sl); }
+// n steps of a stride stay within 2^40 elements, more than any memory, so that no sum of them overflows.
+bool reach_ok(long long s, long long n) { return s >= 0 && s <= (1LL << 40) / n; }
+bool stride_ok(long long s, long long n) { return s % 8 == 0 && s < (1LL << 39) && reach_ok(s, n); }
+bool rows_ok(const Rows &r, int B, int H, int L) {
+  return stride_ok(r.sb, B) && stride_ok(r.sh, H) && r.sh < (1LL << 32) && stride_ok(r.sl, L);
+}
 
 Span rows_span(const Rows &r, int B, int H, int L, int d) {
   if (!r.p) return {nullptr, 0};
@@ -63,7 +67,7 @@ int check_dims(int dtype, int B, int Hq, int Hkv, int L, int d) {
 }
 
 int check_rope(const double *inv_freq, int rotary, float factor, float eps, const int *positions, long long positions_stride,
-               const void *q_weight, const void *k_weight, int Hq, int Hkv, int d) {
+               const void *q_weight, const void *k_weight, int B, int Hq, int Hkv, int d) {
   if (rotary < 0 || rotary > d || rotary % 16 || (rotary > 0 && !inv_freq)) return GBATTN_ERR_ROTARY;
   // Norms: a weight for each tensor that is there, or none.
   const bool norm = q_weight || k_weight;
@@ -71,7 +75,7 @@ int check_rope(const double *inv_freq, int rotary, float factor, float eps, cons
   if (!abi_aligned(inv_freq, 8) || !abi_aligned(positions, 4) || !abi_aligned(q_weight, 16) || !abi_aligned(k_weight, 16))
     return GBATTN_ERR_ALIGN;
   if (!std::isfinite(factor) || !(factor > 0.f) || !finite_nonneg(eps)) return GBATTN_ERR_SCALE;
-  if (positions && positions_stride < 0) return GBATTN_ERR_STRIDE;
+  if (positions && !reach_ok(positions_stride, B)) return GBATTN_ERR_STRIDE;
   return GBATTN_OK;
 }
 
@@ -94,7 +98,7 @@ int check_pages(const void *k, const void *v, long long sp, long long sh, long l
                 long long *extent) {
   if (pages <= 0 || Hkv <= 0) return GBATTN_ERR_DIMS;
   if (page <= 0 || page % 8) return GBATTN_ERR_PAGES;
-  if (!stride_ok(sp) || !stride_ok(sh) || sh >= (1LL << 32) || !stride_ok(ss)) return GBATTN_ERR_STRIDE;
+  if (!stride_ok(sp, pages) || !stride_ok(sh, Hkv) || sh >= (1LL << 32) || !stride_ok(ss, page)) return GBATTN_ERR_STRIDE;
   const long long slots = (page - 1LL) * ss + d, heads = (Hkv - 1LL) * sh + d;
   const bool head_outer = ss >= d && (Hkv == 1 || sh >= slots), slot_outer = (Hkv == 1 || sh >= d) && ss >= heads;
   if (!head_outer && !slot_outer) return GBATTN_ERR_STRIDE;
@@ -158,10 +162,10 @@ extern "C" int attn_rope(const void *q, long long q_sb, long long q_sh, long lon
   if (rc != GBATTN_OK) return rc;
   if (Hq <= 0) return GBATTN_ERR_DIMS;
   if (!abi_aligned(q, 16) || !abi_aligned(k, 16) || !abi_aligned(q_out, 16) || !abi_aligned(k_out, 16)) return GBATTN_ERR_ALIGN;
-  if ((rc = check_rope(inv_freq, rotary, factor, eps, positions, positions_stride, q_weight, k_weight, Hq, Hkv, d)) != GBATTN_OK)
+  if ((rc = check_rope(inv_freq, rotary, factor, eps, positions, positions_stride, q_weight, k_weight, B, Hq, Hkv, d)) != GBATTN_OK)
     return rc;
   const Rows rq{q, q_sb, q_sh, q_sl}, rk{Hkv > 0 ? k : nullptr, k_sb, k_sh, k_sl};
-  if (!rows_ok(rq) || (rk.p && !rows_ok(rk))) return GBATTN_ERR_STRIDE;
+  if (!rows_ok(rq, B, Hq, L) || (rk.p && !rows_ok(rk, B, Hkv, L))) return GBATTN_ERR_STRIDE;
   const long long rows = static_cast<long long>(B) * L;
   const Span out[2] = {dense_span(q_out, rows * Hq * d, 2), dense_span(rk.p ? k_out : nullptr, rows * Hkv * d, 2)};
   const Span in[6] = {rows_span(rq, B, Hq, L, d), rows_span(rk, B, Hkv, L, d), dense_span(inv_freq, rotary / 2, 8),
@@ -206,12 +210,14 @@ extern "C" int attn_rope_bwd(const void *dq_up, long long dq_sb, long long dq_sh
                                 norm ? dk_weight : nullptr, norm ? workspace : nullptr, nullptr};
   for (const void *p : ptrs)
     if (!abi_aligned(p, 16)) return GBATTN_ERR_ALIGN;
-  if ((rc = check_rope(inv_freq, rotary, factor, eps, positions, positions_stride, q_weight, k_weight, Hq, Hkv, d)) != GBATTN_OK)
+  if ((rc = check_rope(inv_freq, rotary, factor, eps, positions, positions_stride, q_weight, k_weight, B, Hq, Hkv, d)) != GBATTN_OK)
     return rc;
   const bool keys = Hkv > 0;
   const Rows gq{dq_up, dq_sb, dq_sh, dq_sl}, gk{keys ? dk_up : nullptr, dk_sb, dk_sh, dk_sl};
   const Rows rq{norm ? q : nullptr, q_sb, q_sh, q_sl}, rk{norm && keys ? k : nullptr, k_sb, k_sh, k_sl};
-  if (!rows_ok(gq) || (gk.p && !rows_ok(gk)) || (rq.p && !rows_ok(rq)) || (rk.p && !rows_ok(rk))) return GBATTN_ERR_STRIDE;
+  if (!rows_ok(gq, B, Hq, L) || (gk.p && !rows_ok(gk, B, Hkv, L)) || (rq.p && !rows_ok(rq, B, Hq, L)) ||
+      (rk.p && !rows_ok(rk, B, Hkv, L)))
+    return GBATTN_ERR_STRIDE;
   const long long rows = static_cast<long long>(B) * L;
   const Span out[5] = {dense_span(dq, rows * Hq * d, 2), dense_span(keys ? dk : nullptr, rows * Hkv * d, 2),
                        dense_span(norm ? dq_weight : nullptr, d, 4), dense_span(norm && keys ? dk_weight : nullptr, d, 4),
@@ -267,9 +273,10 @@ extern "C" int attn_cache_append(const void *k, long long k_sb, long long k_sh, 
   if (!abi_aligned(k, 16) || !abi_aligned(v, 16) || (Hq > 0 && (!abi_aligned(q, 16) || !abi_aligned(q_out, 16))) ||
       !abi_aligned(table, 4) || !abi_aligned(lengths, 4) || !abi_aligned(counts, 4))
     return GBATTN_ERR_ALIGN;
-  if ((rc = check_rope(inv_freq, rotary, factor, eps, nullptr, 0, q_weight, k_weight, Hq, Hkv, d)) != GBATTN_OK) return rc;
+  if ((rc = check_rope(inv_freq, rotary, factor, eps, nullptr, 0, q_weight, k_weight, B, Hq, Hkv, d)) != GBATTN_OK) return rc;
   const Rows rk{k, k_sb, k_sh, k_sl}, rv{v, v_sb, v_sh, v_sl}, rq{Hq > 0 ? q : nullptr, q_sb, q_sh, q_sl};
-  if (!rows_ok(rk) || !rows_ok(rv) || (rq.p && !rows_ok(rq)) || table_stride < 0) return GBATTN_ERR_STRIDE;
+  if (!rows_ok(rk, B, Hkv, L) || !rows_ok(rv, B, Hkv, L) || (rq.p && !rows_ok(rq, B, Hq, L)) || !reach_ok(table_stride, B))
+    return GBATTN_ERR_STRIDE;
   long long extent = 0;
   if ((rc = check_pages(k_pages, v_pages, page_stride, head_stride, slot_stride, pages, page, Hkv, d, &extent)) != GBATTN_OK)
     return rc;
@@ -390,7 +397,7 @@ extern "C" int attn_decode_paged(const void *q, long long q_sb, long long q_sh, 
     return GBATTN_ERR_ALIGN;
   if (!std::isfinite(scale) || !(scale > 0.f)) return GBATTN_ERR_SCALE;
   const Rows rq{q, q_sb, q_sh, 0};
-  if (!rows_ok(rq) || table_stride < 0) return GBATTN_ERR_STRIDE;
+  if (!rows_ok(rq, B, Hq, 1) || !reach_ok(table_stride, B)) return GBATTN_ERR_STRIDE;
   long long extent = 0;
   if ((rc = check_pages(k_pages, v_pages, page_stride, head_stride, slot_stride, pages, page, Hkv, d, &extent)) != GBATTN_OK)
     return rc;

@@ -28,6 +28,8 @@
 // bandwidth: a read-only stream); 16 query heads 307 to 321; d = 64 309 to 315; d = 256 298 to 302; d = 512
 // 316 to 319.  One sequence of 1000 tokens: 9.2 us, the chain of launch, lengths, table, load, two
 // products and the join.
+#include <atomic>
+
 #include "paged_decode.cuh"
 #include "attn_fwd_kernel.cuh"
 #include "ptx_paged.cuh"
@@ -320,8 +322,10 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, NH>::RES)
   if (warp == 4) {
     tmem_alloc(smem_u32(&misc.tmem_base), C::T_COLS);
     tmem_relinquish();
+    // Only now: a dependent kernel's CTA beside this one must not take the tensor memory first and
+    // then wait for this kernel's end.
+    grid_launch_dependents();
   }
-  grid_launch_dependents();
   grid_wait_prior();  // what follows reads the previous kernels' results
 
   // ------------------------------------------------------------ this CTA's share
@@ -881,7 +885,7 @@ template <int D, int NH>
 cudaError_t launch_paged(const PagedLaunch &a) {
   using C = PagedCfg<D, NH>;
   auto *kern = decode_paged_kernel<D, NH>;
-  static unsigned long long configured = 0;  // a bit per device
+  static std::atomic<unsigned long long> configured{0};  // a bit per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

@@ -80,7 +80,11 @@ REFUSED = {
               ("copy", dict(vp=A[12] + 8)), ("decode", dict(q=A[12] + 2)), ("decode", dict(lengths=A[12] + 1))],
     "STRIDE": [("rope", dict(qs=[A[0], 2048, 512, 68])), ("rope", dict(qs=[A[0], -2048, 512, 64])), ("rope", dict(ps=-1)), ("append", dict(ts=-1)),
                ("append", dict(strides=(2048, 1024, 60))), ("copy", dict(strides=(2040, 1024, 64))), ("decode", dict(strides=(0, 1024, 64))),
-               ("decode", dict(strides=(2048, 1024, 0))), ("decode", dict(strides=(2048, 512, 64))), ("decode", dict(qs=(256, 4)))],
+               ("decode", dict(strides=(2048, 1024, 0))), ("decode", dict(strides=(2048, 512, 64))), ("decode", dict(qs=(256, 4))),
+               # offsets that would pass 2^40 elements, and 2^63 with them
+               ("rope", dict(B=1 << 28, L=1, qs=[A[0], 1 << 38, 64, 64])), ("rope", dict(B=1 << 20, ps=1 << 50)), ("append", dict(B=1 << 20, ts=1 << 60)),
+               ("append", dict(page=1 << 30, strides=(1 << 38, 64, 1 << 38))), ("copy", dict(page=1 << 30, Hkv=1 << 30, strides=(1 << 38, 1 << 31, 64))),
+               ("copy", dict(pages=1 << 30, strides=(1 << 38, 1024, 64))), ("decode", dict(ts=1 << 62)), ("decode", dict(B=1 << 27, qs=(1 << 38, 64)))],
     "PAGES": [("append", dict(page=v)) for v in (0, -8, 4, 20)] + [("decode", dict(page=12)), ("copy", dict(page=1)), ("copy", dict(src=(0, 10), dst=(1, 2))),
               ("copy", dict(src=(0,), dst=(-1,)))],
     "HEADS": [("decode", dict(Hq=3)), ("decode", dict(Hq=1))],
