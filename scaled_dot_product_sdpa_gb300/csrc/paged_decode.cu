@@ -23,11 +23,12 @@
 // make several TMA boxes per slot; a producer issues one in about 53 cycles, so the boxes are dealt
 // over three of them (one: pages of 8 tokens 645 us, of 16 454, of 128 302; three: 305, 301, 298).
 //
-// Measured on GB300 (64 sequences x 8 key heads x 8000 tokens, d = 128, bf16; 2.1 GB): 298 to 307 us for
-// pages of 8 to 128 tokens and up to 8 query heads to a key head, 6.8 to 7.0 TB/s (103% of the copy
-// bandwidth: a read-only stream); 16 query heads 307 to 321; d = 64 309 to 315; d = 256 298 to 302; d = 512
-// 316 to 319.  One sequence of 1000 tokens: 9.2 us, the chain of launch, lengths, table, load, two
-// products and the join.
+// Measured on GB300 (64 sequences x 8 key heads x 8000 tokens, d = 128, bf16; 2.1 GB): 296 to 305 us for
+// pages of 8 to 128 tokens and up to 8 query heads to a key head, 7.0 TB/s (103% of the copy
+// bandwidth: a read-only stream); 16 query heads 306 to 320.  The same bytes at d = 64 307 to 315 (16
+// heads 400: softmax and both products of 16 columns take longer than a tile of 64 columns does
+// to arrive), d = 256 298 to 307, d = 512 315 to 319 (16 heads 355).  One sequence of 1000 tokens: 9.2 us, the
+// chain of launch, lengths, table, load, two products and the join.
 #include <atomic>
 
 #include "paged_decode.cuh"
