@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdResident<E>) rope_bwd_kernel
       }
 #pragma unroll
     for (int i = 0; i < U; ++i, dst += step) {
-      const float rstd = rsqrtf(ss[i] * inv_d + p.eps);
+      const float rstd = i < rows_here ? rsqrtf(ss[i] * inv_d + p.eps) : 0.f;  // (infinite for a row of zeros without eps)
       const float mean = gx[i] * rstd * inv_d;  // mean(g xh)
       const uint64_t r = f32x2(rstd, rstd), m = f32x2(-mean, -mean);
 #pragma unroll

@@ -102,6 +102,21 @@ def test_backward_matches_the_formula(B, Hq, Hkv, L, d, rotary, dtype, interleav
         check(got[2 + n], (dy * xh).sum((0, 1, 2)), (size * xh.abs()).sum((0, 1, 2)), "dw", depth=128 + 64)
 
 
+@pytest.mark.parametrize("Hq,Hkv,L,d", [(5, 3, 3, 64), (1, 1, 1, 128), (7, 2, 19, 256), (3, 1, 5, 512)])
+def test_backward_without_eps(Hq, Hkv, L, d):
+    """Threads without a row of their own add nothing to the weights' gradients, although 1 / sqrt(0 + eps) is infinite for them."""
+    q, k, dq, dk = (draw((2, h, L, d), torch.float16, 30 + n) for n, h in enumerate((Hq, Hkv, Hq, Hkv)))
+    wq, wk = draw((d,), torch.float16, 35), draw((d,), torch.float16, 36)
+    got = gb.attn_rope_bwd(dq.cuda(), dk.cuda(), None, q=q.cuda(), k=k.cuda(), q_weight=wq.cuda(), k_weight=wk.cuda(), eps=0.0)
+    for n, (x, up, w) in enumerate(((q, dq, wq), (k, dk, wk))):
+        x, g = x.double(), up.double() * w.double()
+        rstd = x.square().mean(-1, keepdim=True).rsqrt()
+        xh = x * rstd
+        want = rstd * (g - xh * (g * xh).mean(-1, keepdim=True))
+        check(got[n], want, rstd * (g.abs() + xh.abs() * (g * xh).abs().mean(-1, keepdim=True)), "dx")
+        check(got[2 + n], (up.double() * xh).sum((0, 1, 2)), (up.double() * xh).abs().sum((0, 1, 2)), "dw", depth=128 + 64)
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_backward_matches_differences(interleaved):
     """<gradient, direction> against central differences of <forward, upstream gradient> in 64 bits, at the values that the kernel
