@@ -10,16 +10,21 @@
 // sum of squares is a shuffle reduction over the row's lanes.
 //
 // The work is cut into units, a few rows for each thread: a tile of `tokens` consecutive (batch,
-// row) positions times a run of heads of one tensor (q, k or, for the append, v).  As many blocks
-// as fit the GPU at once take equal runs of consecutive units, so that none is left with a thin
-// last wave.  A unit's loads are all issued before its first row is worked on; a new tile's
-// cosines and sines are computed once, into shared memory, behind them, and each thread keeps
-// those of its token in registers.  Arithmetic runs on fp32 pairs (two elements an instruction):
-// with 16 elements a lane and scalar arithmetic, norm and rotation of 4 x 40 x 2048 x 128 in bf16
-// took 44.5 us on GB300 and its backward pass 92 (registers for 2 to 4 warps a scheduler, 180
-// instructions for two rows); now 37.8 (4.5 TB/s) and 63.6 (4.0 TB/s), rotation alone of 100003 x
-// 32 x 64 136 us (6.0 TB/s).  What bounds the norms now is the latency of their chain, loads,
-// reduction, stores, at 24 warps an SM.
+// row) positions times a step, a run of heads of one tensor (q, k or, for the append, v).  As many
+// blocks as fit the GPU at once take equal runs of consecutive units, so that none is left with a
+// thin last wave; a block goes through its tiles, their tensors and their steps, and works out
+// addresses once per tensor.  A unit's loads are all issued before its first row is worked on; a new
+// tile's cosines and sines are computed once, into shared memory, behind them, and each thread keeps
+// those of its token in registers.  Arithmetic runs on fp32 pairs (two elements an instruction).
+//
+// Measured on GB300: rotation of 8 x 64 x 512 x 128 in fp16 25.3 us (5.3 TB/s), of half of each head of
+// 100003 x 32 x 64 134 us (6.1 TB/s); norm and rotation of 4 x 40 x 2048 x 128 in bf16 34.9 us (4.8 TB/s), its
+// backward pass 58.3 (4.3 TB/s); the append of 8 x 48 x 1024 x 128 37.9, with norms 41.2 (5.3, 4.9 TB/s).
+// What bounds the norms is issue (55% of the slots, about 130 instructions for a warp's two rows of
+// 128) and the chain of loads, reduction and stores at 24 warps an SM.  Tried and slower or flat: 16
+// elements a lane without pairs (44.5 and 92 us), addresses worked out per unit (36.6, 62.3), the
+// next unit's loads ahead in registers (39 to 60) or through shared memory by asynchronous copies, two to
+// four units deep (38.4, 62 to 72), smaller shares in two or four waves (36.9 and more).
 //
 // Angles: position x inv_freq is reduced in integers.  inv_freq / 2 pi becomes a 64-bit
 // binary fraction of a turn; its product with the position, taken modulo 2^64, is the angle
@@ -36,8 +41,8 @@ namespace {
 
 // Rows that a thread loads before it works on the first, and blocks that share an SM (the
 // kernels' launch bounds).  Measured on GB300 with 4 rows and 3 blocks against 2 rows and 4 blocks:
-// rotation of 8 x 64 x 512 x 128 26.7 us, 32.3; with norms of 4 x 40 x 2048 x 128 37.8, 46.5.  The
-// backward pass reads twice as much a row: 4 rows and 2 blocks 63.6 us, 2 rows and 3 blocks 70.2.
+// rotation of 8 x 64 x 512 x 128 25.3 us, 33.0; with norms of 4 x 40 x 2048 x 128 34.9, 48.5.  The
+// backward pass reads twice as much a row: 4 rows and 2 blocks 58.3 us, 3 and 2 61.1, 2 and 3 77.7.
 template <int E>
 constexpr int kAtOnce = E == 8 ? 4 : 2;
 template <int E>
@@ -152,7 +157,7 @@ __device__ __forceinline__ void unpack(const Vec<E> &a, const Vec<E> &b, Pairs<E
   }
 }
 template <bool BF, bool INTER, int E>
-__device__ __forceinline__ void store_row(uint16_t *row, const Place &at, const Pairs<E> &x) {
+__device__ __forceinline__ void store_row(uint16_t *row, int over, const Pairs<E> &x) {
   Vec<E> a, b;
 #pragma unroll
   for (int i = 0; i < E / 4; ++i) {
@@ -168,8 +173,8 @@ __device__ __forceinline__ void store_row(uint16_t *row, const Place &at, const 
       b.w[i] = v;
     }
   }
-  store_vec<E>(row + at.c0, a);
-  store_vec<E>(row + at.c1, b);
+  store_vec<E>(row, a);
+  store_vec<E>(row + over, b);
 }
 
 // Cosines, sines and negated sines of a lane's pairs (1, 0 where it does not turn).
@@ -245,26 +250,27 @@ __device__ __forceinline__ void fill_frequencies(Frequencies &f, const RopeParam
     f.factor[i] = isfinite(x) ? p.factor : NAN;
   }
 }
-// The tile's cosines and sines: entry [r][token], r a pair's number.
+// The tile's cosines and sines: a row of a token's pairs after the other, 16 bytes apart so that
+// neither the threads of fill_turns (neighbouring tokens) nor a row's lanes (neighbouring pairs)
+// meet in few banks.
+__host__ __device__ __forceinline__ int turns_row(int rotary) { return (rotary >> 1) + 2; }
 __device__ __forceinline__ void fill_turns(float2 *table, const int *pos, const Frequencies &f, const RopeParams &p) {
   const int shift = 31 - __clz(p.tokens);
   for (int i = threadIdx.x; i < (p.rotary >> 1) << shift; i += kRopeThreads) {
     const int r = i >> shift;
-    table[i] = turn_of(pos[i & (p.tokens - 1)], f.turns[r], f.factor[r], p.sign);
+    const int token = i & (p.tokens - 1);
+    table[token * turns_row(p.rotary) + r] = turn_of(pos[token], f.turns[r], f.factor[r], p.sign);
   }
 }
 template <int E>
-__device__ __forceinline__ void load_turns(const float2 *table, int token, int tokens, const Place &at, Turn<E> &t) {
+__device__ __forceinline__ void load_turns(const float2 *table, int token, int rotary, const Place &at, Turn<E> &t) {
 #pragma unroll
   for (int i = 0; i < E / 4; ++i) {
-    float2 x = make_float2(1.f, 0.f), y = x;
-    if (at.turns) {
-      x = table[(E / 2 * at.lane + 2 * i) * tokens + token];
-      y = table[(E / 2 * at.lane + 2 * i + 1) * tokens + token];
-    }
-    t.c[i] = f32x2(x.x, y.x);
-    t.s[i] = f32x2(x.y, y.y);
-    t.n[i] = f32x2(-x.y, -y.y);
+    float4 x = make_float4(1.f, 0.f, 1.f, 0.f);  // two pairs
+    if (at.turns) x = *reinterpret_cast<const float4 *>(table + token * turns_row(rotary) + E / 2 * at.lane + 2 * i);
+    t.c[i] = f32x2(x.x, x.z);
+    t.s[i] = f32x2(x.y, x.w);
+    t.n[i] = f32x2(-x.y, -x.w);
   }
 }
 
@@ -304,7 +310,7 @@ __device__ __forceinline__ const uint16_t *row_at(const void *p, const Token &t,
 template <bool BF, bool NORM, bool INTER, int E, bool APPEND>
 __global__ void __launch_bounds__(kRopeThreads, kResident<E>) rope_kernel(const RopeParams p) {
   constexpr int U = kAtOnce<E>;
-  extern __shared__ float2 turns[];
+  extern __shared__ __align__(16) float2 turns[];
   __shared__ int pos[kRopeMaxTokens];
   __shared__ long long cell[APPEND ? kRopeMaxTokens : 1];  // element offset of the page slot, -1: none, -2: behind the last token
   __shared__ Frequencies freq;
@@ -319,128 +325,148 @@ __global__ void __launch_bounds__(kRopeThreads, kResident<E>) rope_kernel(const 
   const float inv_d = 1.f / static_cast<float>(p.d);  // exact: a power of two
   if constexpr (NORM) fill_weights<BF, INTER, E>(weights, p);
   fill_frequencies(freq, p);
-  Units u = units_of(p);
-  bool fresh = true, reads = false;
-  Token tok;
-  long long to = 0;
-  Turn<E> turn;
-  for (; u.left > 0; --u.left) {
-    const int n0 = u.tile * p.tokens;
-    if (fresh) {
-      tok = token_of(p, n0 + token);
-      reads = tok.in;
-      if constexpr (APPEND)
-        if (p.counts && tok.in) reads = tok.l < p.counts[tok.b];  // rows behind the last token are not read
-    }
-    // The unit's tensor, heads and source; the same in every thread but for the token.
-    const int kind = u.step < p.steps_q ? 0 : u.step < p.steps_q + p.steps_k ? 1 : 2;
-    const int heads = kind == 0 ? p.Hq : p.Hkv;
-    const int h0 = (u.step - (kind == 0 ? 0 : kind == 1 ? p.steps_q : p.steps_q + p.steps_k)) * groups * p.at_once + group;
-    const uint32_t src_h = static_cast<uint32_t>(kind == 0 ? p.qs[1] : kind == 1 ? p.ks[1] : p.vs[1]);
-    const uint16_t *src = row_at(kind == 0 ? p.q : kind == 1 ? p.k : p.v, tok, kind == 0 ? p.qs[0] : kind == 1 ? p.ks[0] : p.vs[0],
-                                 kind == 0 ? p.qs[2] : kind == 1 ? p.ks[2] : p.vs[2]) +
-                          static_cast<uint64_t>(h0) * src_h;
-    const int rows_here = tok.in && h0 < heads ? min(p.at_once, (heads - h0 + groups - 1) / groups) : 0;  // of this thread
-    Vec<E> a[U], b[U];
-    {
-      const uint64_t step = static_cast<uint64_t>(groups) * src_h;
-      const uint16_t *from = src;
+  const int per = groups * p.at_once;
+  for (Units u = units_of(p); u.left > 0; u.step = 0, ++u.tile) {  // a tile
+    const int n0 = u.tile * p.tokens, stop = min(p.steps, u.step + u.left);
+    u.left -= stop - u.step;
+    const Token tok = token_of(p, n0 + token);
+    bool reads = tok.in, fresh = true;
+    if constexpr (APPEND)
+      if (p.counts && tok.in) reads = tok.l < p.counts[tok.b];  // rows behind the last token are not read
+    long long to = 0;
+    Turn<E> turn;
+    for (int s = u.step; s < stop;) {  // its steps of one tensor
+      const int kind = s < p.steps_q ? 0 : s < p.steps_q + p.steps_k ? 1 : 2;
+      const int heads = kind == 0 ? p.Hq : p.Hkv, first = kind == 0 ? 0 : kind == 1 ? p.steps_q : p.steps_q + p.steps_k;
+      const int end = min(stop, first + (kind == 0 ? p.steps_q : p.steps_k));
+      int h0 = (s - first) * per + group;
+      const uint32_t src_h = static_cast<uint32_t>(kind == 0 ? p.qs[1] : kind == 1 ? p.ks[1] : p.vs[1]);
+      const uint16_t *src = row_at(kind == 0 ? p.q : kind == 1 ? p.k : p.v, tok, kind == 0 ? p.qs[0] : kind == 1 ? p.ks[0] : p.vs[0],
+                                   kind == 0 ? p.qs[2] : kind == 1 ? p.ks[2] : p.vs[2]) +
+                            static_cast<uint64_t>(h0) * src_h + at.c0;
+      const int over = at.c1 - at.c0;
+      const uint64_t src_step = static_cast<uint64_t>(groups) * src_h;
+      const bool paged = APPEND && kind != 0, copies = APPEND && (plain || kind == 2);
+      const uint32_t dst_h = paged ? static_cast<uint32_t>(p.head_s) : out_h;
+      const uint64_t dst_step = static_cast<uint64_t>(groups) * dst_h;
+      uint16_t *dst = static_cast<uint16_t *>(paged ? (kind == 1 ? p.k_pages : p.v_pages) : kind == 0 ? p.q_out : p.k_out) +
+                      static_cast<uint64_t>(h0) * dst_h + at.c0;
+      if (!paged) dst += static_cast<long long>(tok.b) * heads * out_h + static_cast<long long>(tok.l) * p.d;
+      bool placed = !paged;
+      for (; s < end; ++s, h0 += per) {
+        const int rows_here = tok.in && h0 < heads ? min(p.at_once, (heads - h0 + groups - 1) / groups) : 0;  // of this thread
+        Vec<E> a[U], b[U];
+        if (__all_sync(0xffffffffu, reads && rows_here == U)) {
 #pragma unroll
-      for (int i = 0; i < U; ++i, from += step) {
-        a[i] = b[i] = zero_vec<E>();
-        if (reads && i < rows_here) {
-          a[i] = load_vec<E>(from + at.c0);
-          b[i] = load_vec<E>(from + at.c1);
-        }
-      }
-    }
-    if (fresh) {  // the same in every thread
-      fresh = false;
-      __syncthreads();  // the tile before is done with the tables
-      if (threadIdx.x < p.tokens) {
-        const Token t = token_of(p, n0 + threadIdx.x);
-        int x = 0;
-        if constexpr (!APPEND) {
-          if (t.in) x = p.positions ? p.positions[t.b * p.pos_s + t.l] : t.l;
+          for (int i = 0; i < U; ++i, src += src_step) {
+            a[i] = load_vec<E>(src);
+            b[i] = load_vec<E>(src + over);
+          }
         } else {
-          long long cl = -2;
-          if (t.in) {
-            const int len = p.lengths[t.b], count = p.counts ? p.counts[t.b] : p.L;
-            if (count < 0 || count > p.L || len < count || len > static_cast<long long>(p.table_w) * p.page) {
-              atomicCAS(p.status, 0u, kDevBadLength);
-            } else if (t.l < count) {
-              x = len - count + t.l;
-              const int index = x / p.page, page = p.table[t.b * p.table_s + index];
-              cl = -1;
-              if (page < 0 || page >= p.pages)
-                atomicCAS(p.status, 0u, kDevBadPage);
-              else
-                cl = page * p.page_s + static_cast<long long>(x - index * p.page) * p.slot_s;
+#pragma unroll
+          for (int i = 0; i < U; ++i) {
+            a[i] = b[i] = zero_vec<E>();
+            if (reads && i < rows_here) {
+              a[i] = load_vec<E>(src + i * src_step);
+              b[i] = load_vec<E>(src + i * src_step + over);
             }
           }
-          cell[threadIdx.x] = cl;
+          src += p.at_once * src_step;
         }
-        pos[threadIdx.x] = x;
-      }
-      __syncthreads();
-      if (p.rotary > 0) {
-        fill_turns(turns, pos, freq, p);
-        __syncthreads();
-      }
-      load_turns<E>(turns, token, p.tokens, at, turn);
-      if constexpr (APPEND) to = cell[token];
-    }
-    const bool paged = APPEND && kind != 0;
-    const uint32_t dst_h = paged ? static_cast<uint32_t>(p.head_s) : out_h;
-    uint16_t *dst = static_cast<uint16_t *>(paged ? (kind == 1 ? p.k_pages : p.v_pages) : kind == 0 ? p.q_out : p.k_out) +
-                    (paged ? max(to, 0LL) : static_cast<long long>(tok.b) * heads * out_h + static_cast<long long>(tok.l) * p.d) + static_cast<uint64_t>(h0) * dst_h;
-    const bool copies = APPEND && (plain || kind == 2), clears = APPEND && kind == 0 && to == -2;
-    const int stored = APPEND && kind != 0 && to < 0 ? 0 : rows_here;
-    const uint64_t step = static_cast<uint64_t>(groups) * dst_h;
-    if (copies || clears) {
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (i < stored) {
-          store_vec<E>(dst + i * step + at.c0, clears ? zero_vec<E>() : a[i]);
-          store_vec<E>(dst + i * step + at.c1, clears ? zero_vec<E>() : b[i]);
-        }
-    }
-    if (!copies) {  // the same in every thread: the shuffles need whole rows
-      Pairs<E> x[U];
-#pragma unroll
-      for (int i = 0; i < U; ++i) unpack<BF, INTER, E>(a[i], b[i], x[i]);
-      if constexpr (NORM) {
-        Pairs<E> w;
-        weight_pairs<E>(weights + (kind == 0 ? 0 : p.d), at.lane, w);
-        float ss[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) ss[i] = lane_dot<E>(x[i], x[i]);
-        for (int o = 1; o < lpr; o <<= 1)
-#pragma unroll
-          for (int i = 0; i < U; ++i) ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], o);
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const float rstd = rsqrtf(ss[i] * inv_d + p.eps);
-          const uint64_t r = f32x2(rstd, rstd);
-#pragma unroll
-          for (int e = 0; e < E / 4; ++e) {
-            x[i].A[e] = fmul2(fmul2(x[i].A[e], r), w.A[e]);
-            x[i].B[e] = fmul2(fmul2(x[i].B[e], r), w.B[e]);
+        if (fresh) {  // the same in every thread
+          fresh = false;
+          __syncthreads();  // the tile before is done with the tables
+          if (threadIdx.x < p.tokens) {
+            const Token t = token_of(p, n0 + threadIdx.x);
+            int x = 0;
+            if constexpr (!APPEND) {
+              if (t.in) x = p.positions ? p.positions[t.b * p.pos_s + t.l] : t.l;
+            } else {
+              long long cl = -2;
+              if (t.in) {
+                const int len = p.lengths[t.b], count = p.counts ? p.counts[t.b] : p.L;
+                if (count < 0 || count > p.L || len < count || len > static_cast<long long>(p.table_w) * p.page) {
+                  atomicCAS(p.status, 0u, kDevBadLength);
+                } else if (t.l < count) {
+                  x = len - count + t.l;
+                  const int index = x / p.page, page = p.table[t.b * p.table_s + index];
+                  cl = -1;
+                  if (page < 0 || page >= p.pages)
+                    atomicCAS(p.status, 0u, kDevBadPage);
+                  else
+                    cl = page * p.page_s + static_cast<long long>(x - index * p.page) * p.slot_s;
+                }
+              }
+              cell[threadIdx.x] = cl;
+            }
+            pos[threadIdx.x] = x;
           }
+          __syncthreads();
+          if (p.rotary > 0) {
+            fill_turns(turns, pos, freq, p);
+            __syncthreads();
+          }
+          load_turns<E>(turns, token, p.rotary, at, turn);
+          if constexpr (APPEND) to = cell[token];
         }
+        if (!placed) {
+          placed = true;
+          dst += max(to, 0LL);
+        }
+        const bool clears = APPEND && kind == 0 && to == -2;
+        const int stored = paged && to < 0 ? 0 : rows_here;
+        if (copies || clears) {
+#pragma unroll
+          for (int i = 0; i < U; ++i)
+            if (i < stored) {
+              store_vec<E>(dst + i * dst_step, clears ? zero_vec<E>() : a[i]);
+              store_vec<E>(dst + i * dst_step + over, clears ? zero_vec<E>() : b[i]);
+            }
+        }
+        if constexpr (NORM) {
+          if (!copies) {  // the same in every thread: the shuffles need whole rows
+            Pairs<E> x[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) unpack<BF, INTER, E>(a[i], b[i], x[i]);
+            Pairs<E> w;
+            weight_pairs<E>(weights + (kind == 0 ? 0 : p.d), at.lane, w);
+            float ss[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) ss[i] = lane_dot<E>(x[i], x[i]);
+            for (int o = 1; o < lpr; o <<= 1)
+#pragma unroll
+              for (int i = 0; i < U; ++i) ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], o);
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+              const float rstd = rsqrtf(ss[i] * inv_d + p.eps);
+              const uint64_t r = f32x2(rstd, rstd);
+#pragma unroll
+              for (int e = 0; e < E / 4; ++e) {
+                x[i].A[e] = fmul2(fmul2(x[i].A[e], r), w.A[e]);
+                x[i].B[e] = fmul2(fmul2(x[i].B[e], r), w.B[e]);
+              }
+            }
+            if (at.turns)
+#pragma unroll
+              for (int i = 0; i < U; ++i) turn_pairs<E>(x[i], turn);
+            const int out = clears ? 0 : stored;
+            uint16_t *row = dst;
+#pragma unroll
+            for (int i = 0; i < U; ++i, row += dst_step)
+              if (i < out) store_row<BF, INTER, E>(row, over, x[i]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < U; ++i)
+            if (i < (clears || copies ? 0 : stored)) {
+              Pairs<E> x;
+              unpack<BF, INTER, E>(a[i], b[i], x);
+              if (at.turns) turn_pairs<E>(x, turn);
+              store_row<BF, INTER, E>(dst + i * dst_step, over, x);
+            }
+        }
+        dst += p.at_once * dst_step;
       }
-      if (at.turns)
-#pragma unroll
-        for (int i = 0; i < U; ++i) turn_pairs<E>(x[i], turn);
-      const int out = clears ? 0 : stored;
-#pragma unroll
-      for (int i = 0; i < U; ++i, dst += step)
-        if (i < out) store_row<BF, INTER, E>(dst, at, x[i]);
-    }
-    if (++u.step == p.steps) {
-      u.step = 0;
-      ++u.tile;
-      fresh = true;
     }
   }
 }
@@ -451,7 +477,7 @@ __global__ void __launch_bounds__(kRopeThreads, kResident<E>) rope_kernel(const 
 template <bool BF, bool INTER, int E>
 __global__ void __launch_bounds__(kRopeThreads, kBwdResident<E>) rope_bwd_kernel(const RopeParams p) {
   constexpr int U = kBwdAtOnce<E>;
-  extern __shared__ float2 turns[];
+  extern __shared__ __align__(16) float2 turns[];
   __shared__ int pos[kRopeMaxTokens];
   __shared__ Frequencies freq;
   __shared__ __align__(16) float weights[1024];
@@ -483,108 +509,106 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdResident<E>) rope_bwd_kernel
   for (int e = 0; e < E; ++e) sums[0][e][threadIdx.x] = sums[1][e][threadIdx.x] = 0.f;
 #pragma unroll
   for (int e = 0; e < E / 4; ++e) dw.A[e] = dw.B[e] = 0ull;
-  bool last_q = true;
-  Units u = units_of(p);
-  bool fresh = true;
-  Token tok;
-  Turn<E> turn;
-  for (; u.left > 0; --u.left) {
-    const int n0 = u.tile * p.tokens;
-    if (fresh) tok = token_of(p, n0 + token);
-    const bool is_q = u.step < p.steps_q;
-    if (is_q != last_q) add_up(last_q ? 0 : 1);
-    last_q = is_q;
-    const int heads = is_q ? p.Hq : p.Hkv;
-    const int h0 = (u.step - (is_q ? 0 : p.steps_q)) * groups * p.at_once + group;
-    const uint32_t x_h = static_cast<uint32_t>(is_q ? p.qs[1] : p.ks[1]), up_h = static_cast<uint32_t>(is_q ? p.dqs[1] : p.dks[1]);
-    const uint16_t *const src =
-        row_at(is_q ? p.q : p.k, tok, is_q ? p.qs[0] : p.ks[0], is_q ? p.qs[2] : p.ks[2]) + static_cast<uint64_t>(h0) * x_h;
-    const uint16_t *const up =
-        row_at(is_q ? p.dq : p.dk, tok, is_q ? p.dqs[0] : p.dks[0], is_q ? p.dqs[2] : p.dks[2]) + static_cast<uint64_t>(h0) * up_h;
-    const int rows_here = tok.in && h0 < heads ? min(p.at_once, (heads - h0 + groups - 1) / groups) : 0;  // of this thread
-    Vec<E> a[U], b[U], da[U], db[U];
-    {
+  const int per = groups * p.at_once, over = at.c1 - at.c0;
+  const uint64_t out_step = static_cast<uint64_t>(groups) * out_h;
+  for (Units u = units_of(p); u.left > 0; u.step = 0, ++u.tile) {  // a tile
+    const int n0 = u.tile * p.tokens, stop = min(p.steps, u.step + u.left);
+    u.left -= stop - u.step;
+    const Token tok = token_of(p, n0 + token);
+    bool fresh = true;
+    Turn<E> turn;
+    for (int s = u.step; s < stop;) {  // its steps of one tensor
+      const bool is_q = s < p.steps_q;
+      const int heads = is_q ? p.Hq : p.Hkv, first = is_q ? 0 : p.steps_q, end = min(stop, first + (is_q ? p.steps_q : p.steps_k));
+      int h0 = (s - first) * per + group;
+      const uint32_t x_h = static_cast<uint32_t>(is_q ? p.qs[1] : p.ks[1]), up_h = static_cast<uint32_t>(is_q ? p.dqs[1] : p.dks[1]);
+      const uint16_t *src = row_at(is_q ? p.q : p.k, tok, is_q ? p.qs[0] : p.ks[0], is_q ? p.qs[2] : p.ks[2]) +
+                            static_cast<uint64_t>(h0) * x_h + at.c0;
+      const uint16_t *up = row_at(is_q ? p.dq : p.dk, tok, is_q ? p.dqs[0] : p.dks[0], is_q ? p.dqs[2] : p.dks[2]) +
+                           static_cast<uint64_t>(h0) * up_h + at.c0;
       const uint64_t step = static_cast<uint64_t>(groups) * x_h, up_step = static_cast<uint64_t>(groups) * up_h;
-      const uint16_t *from = src, *grad = up;
+      uint16_t *dst = static_cast<uint16_t *>(is_q ? p.q_out : p.k_out) + static_cast<long long>(tok.b) * heads * out_h +
+                      static_cast<long long>(tok.l) * p.d + static_cast<uint64_t>(h0) * out_h + at.c0;
+      for (; s < end; ++s, h0 += per, dst += p.at_once * out_step) {
+        const int rows_here = tok.in && h0 < heads ? min(p.at_once, (heads - h0 + groups - 1) / groups) : 0;  // of this thread
+        Vec<E> a[U], b[U], da[U], db[U];
 #pragma unroll
-      for (int i = 0; i < U; ++i, from += step, grad += up_step) {
-        a[i] = b[i] = da[i] = db[i] = zero_vec<E>();
-        if (i < rows_here) {
-          a[i] = load_vec<E>(from + at.c0);
-          b[i] = load_vec<E>(from + at.c1);
-          da[i] = load_vec<E>(grad + at.c0);
-          db[i] = load_vec<E>(grad + at.c1);
+        for (int i = 0; i < U; ++i) {
+          a[i] = b[i] = da[i] = db[i] = zero_vec<E>();
+          if (i < rows_here) {
+            a[i] = load_vec<E>(src + i * step);
+            b[i] = load_vec<E>(src + i * step + over);
+            da[i] = load_vec<E>(up + i * up_step);
+            db[i] = load_vec<E>(up + i * up_step + over);
+          }
+        }
+        src += p.at_once * step;
+        up += p.at_once * up_step;
+        if (fresh) {
+          fresh = false;
+          __syncthreads();
+          if (threadIdx.x < p.tokens) {
+            const Token t = token_of(p, n0 + threadIdx.x);
+            pos[threadIdx.x] = !t.in ? 0 : p.positions ? p.positions[t.b * p.pos_s + t.l] : t.l;
+          }
+          __syncthreads();
+          if (p.rotary > 0) {
+            fill_turns(turns, pos, freq, p);
+            __syncthreads();
+          }
+          load_turns<E>(turns, token, p.rotary, at, turn);
+        }
+        Pairs<E> w;
+        weight_pairs<E>(weights + (is_q ? 0 : p.d), at.lane, w);
+        uint16_t *row = dst;
+        Pairs<E> g[U];
+        float ss[U], gx[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) unpack<BF, INTER, E>(da[i], db[i], g[i]);
+        if (at.turns)
+#pragma unroll
+          for (int i = 0; i < U; ++i) turn_pairs<E>(g[i], turn);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          Pairs<E> x, gw;
+          unpack<BF, INTER, E>(a[i], b[i], x);
+#pragma unroll
+          for (int e = 0; e < E / 4; ++e) {
+            gw.A[e] = fmul2(g[i].A[e], w.A[e]);
+            gw.B[e] = fmul2(g[i].B[e], w.B[e]);
+          }
+          ss[i] = lane_dot<E>(x, x);
+          gx[i] = lane_dot<E>(gw, x);
+        }
+        for (int o = 1; o < lpr; o <<= 1)
+#pragma unroll
+          for (int i = 0; i < U; ++i) {
+            ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], o);
+            gx[i] += __shfl_xor_sync(0xffffffffu, gx[i], o);
+          }
+#pragma unroll
+        for (int i = 0; i < U; ++i, row += out_step) {
+          const float rstd = i < rows_here ? rsqrtf(ss[i] * inv_d + p.eps) : 0.f;  // (infinite for a row of zeros without eps)
+          const float mean = gx[i] * rstd * inv_d;  // mean(g xh)
+          const uint64_t r = f32x2(rstd, rstd), m = f32x2(-mean, -mean);
+          Pairs<E> x;  // unpacked again: a register for a word rather than two
+#pragma unroll
+          for (int e = 0; e < E / 4; ++e) asm volatile("" : "+r"(a[i].w[e]), "+r"(b[i].w[e]));
+          unpack<BF, INTER, E>(a[i], b[i], x);
+#pragma unroll
+          for (int e = 0; e < E / 4; ++e) {
+            const uint64_t ha = fmul2(x.A[e], r), hb = fmul2(x.B[e], r);
+            dw.A[e] = ffma2(g[i].A[e], ha, dw.A[e]);
+            dw.B[e] = ffma2(g[i].B[e], hb, dw.B[e]);
+            x.A[e] = fmul2(r, ffma2(ha, m, fmul2(g[i].A[e], w.A[e])));
+            x.B[e] = fmul2(r, ffma2(hb, m, fmul2(g[i].B[e], w.B[e])));
+          }
+          if (i < rows_here) store_row<BF, INTER, E>(row, over, x);
         }
       }
-    }
-    if (fresh) {
-      fresh = false;
-      __syncthreads();
-      if (threadIdx.x < p.tokens) {
-        const Token t = token_of(p, n0 + threadIdx.x);
-        pos[threadIdx.x] = !t.in ? 0 : p.positions ? p.positions[t.b * p.pos_s + t.l] : t.l;
-      }
-      __syncthreads();
-      if (p.rotary > 0) {
-        fill_turns(turns, pos, freq, p);
-        __syncthreads();
-      }
-      load_turns<E>(turns, token, p.tokens, at, turn);
-    }
-    uint16_t *dst = static_cast<uint16_t *>(is_q ? p.q_out : p.k_out) + static_cast<long long>(tok.b) * heads * out_h +
-                    static_cast<long long>(tok.l) * p.d + static_cast<uint64_t>(h0) * out_h;
-    Pairs<E> w;
-    weight_pairs<E>(weights + (is_q ? 0 : p.d), at.lane, w);
-    const uint64_t step = static_cast<uint64_t>(groups) * out_h;
-    Pairs<E> x[U], g[U];
-    float ss[U], gx[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      unpack<BF, INTER, E>(a[i], b[i], x[i]);
-      unpack<BF, INTER, E>(da[i], db[i], g[i]);
-    }
-    if (at.turns)
-#pragma unroll
-      for (int i = 0; i < U; ++i) turn_pairs<E>(g[i], turn);
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      Pairs<E> gw;
-#pragma unroll
-      for (int e = 0; e < E / 4; ++e) {
-        gw.A[e] = fmul2(g[i].A[e], w.A[e]);
-        gw.B[e] = fmul2(g[i].B[e], w.B[e]);
-      }
-      ss[i] = lane_dot<E>(x[i], x[i]);
-      gx[i] = lane_dot<E>(gw, x[i]);
-    }
-    for (int o = 1; o < lpr; o <<= 1)
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], o);
-        gx[i] += __shfl_xor_sync(0xffffffffu, gx[i], o);
-      }
-#pragma unroll
-    for (int i = 0; i < U; ++i, dst += step) {
-      const float rstd = i < rows_here ? rsqrtf(ss[i] * inv_d + p.eps) : 0.f;  // (infinite for a row of zeros without eps)
-      const float mean = gx[i] * rstd * inv_d;  // mean(g xh)
-      const uint64_t r = f32x2(rstd, rstd), m = f32x2(-mean, -mean);
-#pragma unroll
-      for (int e = 0; e < E / 4; ++e) {
-        const uint64_t ha = fmul2(x[i].A[e], r), hb = fmul2(x[i].B[e], r);
-        dw.A[e] = ffma2(g[i].A[e], ha, dw.A[e]);
-        dw.B[e] = ffma2(g[i].B[e], hb, dw.B[e]);
-        x[i].A[e] = fmul2(r, ffma2(ha, m, fmul2(g[i].A[e], w.A[e])));
-        x[i].B[e] = fmul2(r, ffma2(hb, m, fmul2(g[i].B[e], w.B[e])));
-      }
-      if (i < rows_here) store_row<BF, INTER, E>(dst, at, x[i]);
-    }
-    if (++u.step == p.steps) {
-      u.step = 0;
-      ++u.tile;
-      fresh = true;
+      add_up(is_q ? 0 : 1);
     }
   }
-  add_up(last_q ? 0 : 1);
   __syncthreads();
   // Lane j's element e (A's, then B's) of every row of threads.
   float *const part = p.parts + static_cast<size_t>(blockIdx.x) * 2 * p.d;
@@ -656,7 +680,7 @@ int plan(RopeParams &p, bool append, int blocks, int at_once) {
   return static_cast<int>(std::min<long long>(p.units, blocks));
 }
 
-size_t turns_bytes(const RopeParams &p) { return static_cast<size_t>(p.tokens) * (p.rotary / 2) * sizeof(float2); }
+size_t turns_bytes(const RopeParams &p) { return p.rotary ? static_cast<size_t>(p.tokens) * turns_row(p.rotary) * sizeof(float2) : 0; }
 
 // The instance for a call's type, norm, layout and head_dim.
 template <bool APPEND>
