@@ -20,7 +20,7 @@
 // Measured on GB300: rotation of 8 x 64 x 512 x 128 in fp16 25.3 us (5.3 TB/s), of half of each head of
 // 100003 x 32 x 64 134 us (6.1 TB/s); norm and rotation of 4 x 40 x 2048 x 128 in bf16 34.9 us (4.8 TB/s), its
 // backward pass 58.3 (4.3 TB/s); the append of 8 x 48 x 1024 x 128 37.9, with norms 41.2 (5.3, 4.9 TB/s).
-// What bounds the norms is issue (55% of the slots, about 130 instructions for a warp's two rows of
+// What bounds the norms is issue (57% of the slots, 127 instructions for a warp's two rows of
 // 128) and the chain of loads, reduction and stores at 24 warps an SM.  Tried and slower or flat: 16
 // elements a lane without pairs (44.5 and 92 us), addresses worked out per unit (36.6, 62.3), the
 // next unit's loads ahead in registers (39 to 60) or through shared memory by asynchronous copies, two to
