@@ -19,7 +19,7 @@
 //
 // Measured on GB300: rotation of 8 x 64 x 512 x 128 in fp16 25.3 us (5.3 TB/s), of half of each head of
 // 100003 x 32 x 64 134 us (6.1 TB/s); norm and rotation of 4 x 40 x 2048 x 128 in bf16 34.9 us (4.8 TB/s), its
-// backward pass 58.3 (4.3 TB/s); the append of 8 x 48 x 1024 x 128 37.9, with norms 41.2 (5.3, 4.9 TB/s).
+// backward pass 57.5 (4.4 TB/s); the append of 8 x 48 x 1024 x 128 37.9, with norms 41.2 (5.3, 4.9 TB/s).
 // What bounds the norms is issue (57% of the slots, 127 instructions for a warp's two rows of
 // 128) and the chain of loads, reduction and stores at 24 warps an SM.  Tried and slower or flat: 16
 // elements a lane without pairs (44.5 and 92 us), addresses worked out per unit (36.6, 62.3), the
@@ -31,6 +31,7 @@
 // modulo one turn, wrong by at most (1 + inv_freq / 4) |position| 2^-64 turns (so a position
 // of 10^6 costs no accuracy, where an fp32 product would be off by 0.06 radians).
 #include <algorithm>
+#include <type_traits>
 
 #include "ptx_paged.cuh"
 #include "rope.cuh"
@@ -42,15 +43,16 @@ namespace {
 // Rows that a thread loads before it works on the first, and blocks that share an SM (the
 // kernels' launch bounds).  Measured on GB300 with 4 rows and 3 blocks against 2 rows and 4 blocks:
 // rotation of 8 x 64 x 512 x 128 25.3 us, 33.0; with norms of 4 x 40 x 2048 x 128 34.9, 48.5.  The
-// backward pass reads twice as much a row: 4 rows and 2 blocks 58.3 us, 3 and 2 61.1, 2 and 3 77.7.
+// backward pass reads twice as much a row: 4 rows and 2 blocks 57.5 us, 3 and 2 61.1, 2 and 3 77.7.
+// With 16 elements a lane (8 x 32 x 106 x 512, and one head of 40495 rows): 2 rows and 2 blocks 32.8 and
+// 113 us, 2 and 1 32.2 and 143, 1 and 2 33.5 and 99.5.
 template <int E>
 constexpr int kAtOnce = E == 8 ? 4 : 2;
 template <int E>
 constexpr int kResident = E == 8 ? 3 : 2;
 template <int E>
-constexpr int kBwdAtOnce = E == 8 ? 4 : 1;
-template <int E>
-constexpr int kBwdResident = E == 8 ? 2 : 1;
+constexpr int kBwdAtOnce = E == 8 ? 4 : 2;
+constexpr int kBwdResident = 2;
 
 // frac(x / 2 pi) 2^64 of a finite double x = m 2^e (m an integer of at most 53 bits):
 // m C 2^(e - 2) with C = 2^66 / 2 pi, as a 128-bit integer, modulo 2^64.
@@ -287,6 +289,21 @@ __device__ __forceinline__ Units units_of(const RopeParams &p) {
   return u;
 }
 
+// f of a constant number of rows, the least of U, U / 2 and 1 that is not below n (the same in every
+// thread): a step of few heads is not worked on as if it had all its rows (backward pass of 2 heads of 25 x
+// 8169 x 64 132.9 us, now 105.1; the forward pass has less to save and pays in registers: 4 x 40 x 2048 x
+// 128 34.9, 36.2).
+template <int U, typename F>
+__device__ __forceinline__ void on_rows(int n, const F &f) {
+  if constexpr (U > 2) {
+    if (n <= 1) return f(std::integral_constant<int, 1>());
+  }
+  if constexpr (U > 1) {
+    if (n <= U / 2) return f(std::integral_constant<int, U / 2>());
+  }
+  f(std::integral_constant<int, U>());
+}
+
 // A thread's token in the current tile.
 struct Token {
   int b, l;
@@ -475,7 +492,7 @@ __global__ void __launch_bounds__(kRopeThreads, kResident<E>) rope_kernel(const 
 // g = dy w:   dx = rstd (g - xh mean(g xh)),   dw += dy xh.  Each block leaves its part of the
 // weights' gradients in parts[block][q, k][d], which rope_dw_kernel adds up in a fixed order.
 template <bool BF, bool INTER, int E>
-__global__ void __launch_bounds__(kRopeThreads, kBwdResident<E>) rope_bwd_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kBwdResident) rope_bwd_kernel(const RopeParams p) {
   constexpr int U = kBwdAtOnce<E>;
   extern __shared__ __align__(16) float2 turns[];
   __shared__ int pos[kRopeMaxTokens];
@@ -510,6 +527,7 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdResident<E>) rope_bwd_kernel
 #pragma unroll
   for (int e = 0; e < E / 4; ++e) dw.A[e] = dw.B[e] = 0ull;
   const int per = groups * p.at_once, over = at.c1 - at.c0;
+  auto rows_of_step = [&](int heads, int i) { return min(p.at_once, (heads - i * per + groups - 1) / groups); };  // of group 0, the most
   const uint64_t out_step = static_cast<uint64_t>(groups) * out_h;
   for (Units u = units_of(p); u.left > 0; u.step = 0, ++u.tile) {  // a tile
     const int n0 = u.tile * p.tokens, stop = min(p.steps, u.step + u.left);
@@ -558,53 +576,56 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdResident<E>) rope_bwd_kernel
           }
           load_turns<E>(turns, token, p.rotary, at, turn);
         }
-        Pairs<E> w;
-        weight_pairs<E>(weights + (is_q ? 0 : p.d), at.lane, w);
-        uint16_t *row = dst;
-        Pairs<E> g[U];
-        float ss[U], gx[U];
+        on_rows<U>(rows_of_step(heads, s - first), [&](auto rows) {
+          constexpr int R = rows.value;
+          Pairs<E> w;
+          weight_pairs<E>(weights + (is_q ? 0 : p.d), at.lane, w);
+          uint16_t *row = dst;
+          Pairs<E> g[R];
+          float ss[R], gx[R];
 #pragma unroll
-        for (int i = 0; i < U; ++i) unpack<BF, INTER, E>(da[i], db[i], g[i]);
-        if (at.turns)
+          for (int i = 0; i < R; ++i) unpack<BF, INTER, E>(da[i], db[i], g[i]);
+          if (at.turns)
 #pragma unroll
-          for (int i = 0; i < U; ++i) turn_pairs<E>(g[i], turn);
+            for (int i = 0; i < R; ++i) turn_pairs<E>(g[i], turn);
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-          Pairs<E> x, gw;
-          unpack<BF, INTER, E>(a[i], b[i], x);
+          for (int i = 0; i < R; ++i) {
+            Pairs<E> x, gw;
+            unpack<BF, INTER, E>(a[i], b[i], x);
 #pragma unroll
-          for (int e = 0; e < E / 4; ++e) {
-            gw.A[e] = fmul2(g[i].A[e], w.A[e]);
-            gw.B[e] = fmul2(g[i].B[e], w.B[e]);
+            for (int e = 0; e < E / 4; ++e) {
+              gw.A[e] = fmul2(g[i].A[e], w.A[e]);
+              gw.B[e] = fmul2(g[i].B[e], w.B[e]);
+            }
+            ss[i] = lane_dot<E>(x, x);
+            gx[i] = lane_dot<E>(gw, x);
           }
-          ss[i] = lane_dot<E>(x, x);
-          gx[i] = lane_dot<E>(gw, x);
-        }
-        for (int o = 1; o < lpr; o <<= 1)
+          for (int o = 1; o < lpr; o <<= 1)
 #pragma unroll
-          for (int i = 0; i < U; ++i) {
-            ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], o);
-            gx[i] += __shfl_xor_sync(0xffffffffu, gx[i], o);
+            for (int i = 0; i < R; ++i) {
+              ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], o);
+              gx[i] += __shfl_xor_sync(0xffffffffu, gx[i], o);
+            }
+#pragma unroll
+          for (int i = 0; i < R; ++i, row += out_step) {
+            const float rstd = i < rows_here ? rsqrtf(ss[i] * inv_d + p.eps) : 0.f;  // (infinite for a row of zeros without eps)
+            const float mean = gx[i] * rstd * inv_d;  // mean(g xh)
+            const uint64_t r = f32x2(rstd, rstd), m = f32x2(-mean, -mean);
+            Pairs<E> x;  // unpacked again: a register for a word rather than two
+#pragma unroll
+            for (int e = 0; e < E / 4; ++e) asm volatile("" : "+r"(a[i].w[e]), "+r"(b[i].w[e]));
+            unpack<BF, INTER, E>(a[i], b[i], x);
+#pragma unroll
+            for (int e = 0; e < E / 4; ++e) {
+              const uint64_t ha = fmul2(x.A[e], r), hb = fmul2(x.B[e], r);
+              dw.A[e] = ffma2(g[i].A[e], ha, dw.A[e]);
+              dw.B[e] = ffma2(g[i].B[e], hb, dw.B[e]);
+              x.A[e] = fmul2(r, ffma2(ha, m, fmul2(g[i].A[e], w.A[e])));
+              x.B[e] = fmul2(r, ffma2(hb, m, fmul2(g[i].B[e], w.B[e])));
+            }
+            if (i < rows_here) store_row<BF, INTER, E>(row, over, x);
           }
-#pragma unroll
-        for (int i = 0; i < U; ++i, row += out_step) {
-          const float rstd = i < rows_here ? rsqrtf(ss[i] * inv_d + p.eps) : 0.f;  // (infinite for a row of zeros without eps)
-          const float mean = gx[i] * rstd * inv_d;  // mean(g xh)
-          const uint64_t r = f32x2(rstd, rstd), m = f32x2(-mean, -mean);
-          Pairs<E> x;  // unpacked again: a register for a word rather than two
-#pragma unroll
-          for (int e = 0; e < E / 4; ++e) asm volatile("" : "+r"(a[i].w[e]), "+r"(b[i].w[e]));
-          unpack<BF, INTER, E>(a[i], b[i], x);
-#pragma unroll
-          for (int e = 0; e < E / 4; ++e) {
-            const uint64_t ha = fmul2(x.A[e], r), hb = fmul2(x.B[e], r);
-            dw.A[e] = ffma2(g[i].A[e], ha, dw.A[e]);
-            dw.B[e] = ffma2(g[i].B[e], hb, dw.B[e]);
-            x.A[e] = fmul2(r, ffma2(ha, m, fmul2(g[i].A[e], w.A[e])));
-            x.B[e] = fmul2(r, ffma2(hb, m, fmul2(g[i].B[e], w.B[e])));
-          }
-          if (i < rows_here) store_row<BF, INTER, E>(row, over, x);
-        }
+        });
       }
       add_up(is_q ? 0 : 1);
     }
@@ -666,7 +687,7 @@ cudaError_t launch(void (*kern)(A...), dim3 grid, int threads, size_t smem, cuda
 int plan(RopeParams &p, bool append, int blocks, int at_once) {
   const long long N = static_cast<long long>(p.B) * p.L;
   const int rows = kRopeThreads / (p.d > 256 ? p.d / 16 : p.d / 8);
-  const int most = p.d > 256 ? 4 : std::min(kRopeMaxTokens, rows);  // d = 512: the angles' table stays at 8 KB
+  const int most = std::min(kRopeMaxTokens, rows);
   p.tokens = 1;
   while (2 * p.tokens <= most && (2LL * p.tokens * blocks <= N || (p.tokens < 4 && p.tokens < N))) p.tokens *= 2;
   for (p.at_once = at_once;; p.at_once >>= 1) {
@@ -715,7 +736,7 @@ cudaError_t launch_append(RopeLaunch &a) { return launch_rows<true>(a); }
 
 cudaError_t launch_rope_bwd(RopeLaunch &a) {
   const bool wide = a.p.d > 256;
-  const int blocks = a.sm_count * (wide ? kBwdResident<16> : kBwdResident<8>);
+  const int blocks = a.sm_count * kBwdResident;
   const int grid = plan(a.p, false, std::min(kRopeMaxParts, blocks), wide ? kBwdAtOnce<16> : kBwdAtOnce<8>);
   const cudaError_t e =
       launch(pick_bwd(a.bf16, a.interleaved, a.p.d), dim3(grid), kRopeThreads, turns_bytes(a.p), a.stream, RopeParams(a.p));
