@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, NH>::RES)
     Seg s;
     uint32_t i = 0;  // tiles done
     for (uint32_t seg = 0; w.next(s); ++seg) {
-      const int block = s.hv % p.blocks, heads = min(NH, p.G - block * NH);
+      const int kv = p.blocks == 1 ? s.hv : s.hv / p.blocks, block = s.hv - kv * p.blocks, heads = min(NH, p.G - block * NH);
       const uint32_t o_at = lanes + C::T_O + (seg & 1) * (C::NO * C::NP);
       float m[NH], l[NH];
 #pragma unroll
@@ -783,9 +783,9 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, NH>::RES)
           // thread: 154 x 32 heads of 4 tokens x 128 82.8 us, now 56.9).  Whatever lies behind the last token in its group (unwritten
           // slots, earlier tiles) times a weight of zero must be zero: clear those rows of V, eight
           // threads to a row.
-          if (!C::ONE) {
+          if constexpr (C::NSLOT < 3 * C::NC) {
             // The slots' earlier loads, of V(i - 1) and K(i + 1), must be past, or a wait for V's load
-            // would take the phase before theirs for it.
+            // would take the phase before theirs for it.  (In a longer ring they were of K(i) at the latest.)
             if (i >= 1) wait_pv(i - 1);
             if (i + 1 < tiles) wait_s(i + 1);
           }
@@ -818,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, NH>::RES)
       due.begins = s.tile == 0;
       due.last = i - 1;
       due.seg = seg;
-      due.row0 = static_cast<size_t>(s.b) * p.Hq + (s.hv / p.blocks) * p.G + block * NH;
+      due.row0 = static_cast<size_t>(s.b) * p.Hq + kv * p.G + block * NH;
       if (!due.whole && due.begins) {
         // The row goes on in the next CTAs: up to the one whose share holds its last unit `end`, the
         // largest c with floor(total c / G) <= end, that is c < (end + 1) G / total.

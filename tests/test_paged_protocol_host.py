@@ -194,9 +194,9 @@ def test_ring_protocol(nc, nslot, nqb, seed):
                     yield
                 assert order == list(range(t))
             if tail[t]:
-                while nc > 1 and t >= 1 and not pv_done(t - 1):
+                while nslot < 3 * nc and t >= 1 and not pv_done(t - 1):
                     yield
-                while nc > 1 and t + 1 < T and not s_there(t + 1):
+                while nslot < 3 * nc and t + 1 < T and not s_there(t + 1):
                     yield
                 for c in range(nc):
                     x = v_pos(t, T, nc) + c
