@@ -837,19 +837,36 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, NH>::RES)
   if (warp == 4) tmem_dealloc(tmem, C::T_COLS);
 }
 
-// Joins the rows that were cut: block (c, h) the h-th head of the row that CTA c's share ends in.
-// W groups of 128 threads, a thread to a column, take every W-th part each.
+// Joins the rows that were cut: block (c, h) the h-th head of the row that CTA c's share ends in, or
+// (W > 1: few rows) block (r, h) that of row r, whose CTA it looks up.  W groups of 128 threads, a thread
+// to a column, take every W-th part each.
 template <int D, int NH, int W>
-__global__ void __launch_bounds__(128 * W) paged_merge_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(128 * W) paged_merge_kernel(const PagedParams p, const int ctas) {
   __shared__ float weight[kPagedMaxCtas];
   __shared__ float sums[W > 1 ? W - 1 : 1][128];
   __shared__ float shared_sum;
   grid_launch_dependents();
   grid_wait_prior();
-  const PagedRecord r = p.records[blockIdx.x];
   const int h = blockIdx.y, tid = threadIdx.x;
+  int cta = blockIdx.x;
+  if constexpr (W > 1) {
+    __shared__ int found;
+    static_assert(128 * W >= kPagedMaxCtas, "a thread to a record");
+    if (tid == 0) found = -1;
+    __syncthreads();
+    const int hvs = p.Hkv * p.blocks, b = blockIdx.x / hvs, hv = blockIdx.x - b * hvs, kv = hv / p.blocks;
+    const int head = b * p.Hq + kv * p.G + (hv - kv * p.blocks) * NH;
+    if (tid < ctas) {
+      const PagedRecord r = p.records[tid];
+      if (r.parts > 0 && r.head == head) found = tid;
+    }
+    __syncthreads();
+    cta = found;
+    if (cta < 0) return;
+  }
+  const PagedRecord r = p.records[cta];
   if (h >= r.heads) return;
-  auto part = [&](int i) -> size_t { return i == 0 ? 2 * static_cast<size_t>(blockIdx.x) + 1 : 2 * (static_cast<size_t>(blockIdx.x) + i); };
+  auto part = [&](int i) -> size_t { return i == 0 ? 2 * static_cast<size_t>(cta) + 1 : 2 * (static_cast<size_t>(cta) + i); };
   for (int i = tid; i < r.parts; i += 128 * W) weight[i] = p.part_lse[part(i) * NH + h];
   __syncthreads();
   if (tid < 32) {
@@ -932,14 +949,15 @@ cudaError_t launch_paged(const PagedLaunch &a) {
   if (!cut) p.records = nullptr;
   e = cudaLaunchKernelEx(&cfg, kern, a.tm_q, a.tm_k, a.tm_v, p);
   if (e != cudaSuccess || !cut) return e;
-  // Rows of eight parts and more are joined by eight groups: one key head of a sequence of 34346 tokens,
-  // 269 parts, 26.0 us with one group and 13.2 with eight; most blocks have nothing to join and end at
-  // once, but with many rows of few parts the wider ones would come in more waves.
-  const bool wide = 8LL * a.p.B * a.p.Hkv * a.p.blocks <= grid;
-  cfg.gridDim = dim3(grid, static_cast<unsigned>(std::min(NH, a.p.G)));
+  // Rows of eight parts and more are joined by eight groups, in blocks for the rows only: one key head of
+  // a sequence of 34346 tokens, 269 parts, 26.0 us with one group, 13.6 with eight (16 query heads to each of 8
+  // key heads, 20000 tokens: 21.8; with a block for every CTA and head, most of them with nothing to do, 24.3).
+  const long long rows = static_cast<long long>(a.p.B) * a.p.Hkv * a.p.blocks;
+  const bool wide = 8 * rows <= grid;
+  cfg.gridDim = dim3(wide ? static_cast<unsigned>(rows) : grid, static_cast<unsigned>(std::min(NH, a.p.G)));
   cfg.blockDim = dim3(wide ? 1024 : 128);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, wide ? paged_merge_kernel<D, NH, 8> : paged_merge_kernel<D, NH, 1>, p);
+  return cudaLaunchKernelEx(&cfg, wide ? paged_merge_kernel<D, NH, 8> : paged_merge_kernel<D, NH, 1>, p, static_cast<int>(grid));
 }
 
 template <int D>

@@ -74,7 +74,7 @@ def v_pos(t, T, nc):
     return (min(t + 2, T) + t) * nc
 
 
-@pytest.mark.parametrize("nc,nslot,nqb", [(1, 12, 2), (1, 11, 2), (1, 6, 2), (1, 5, 2), (2, 6, 2), (2, 5, 2), (2, 5, 1), (2, 4, 1), (4, 6, 2), (4, 5, 2)])
+@pytest.mark.parametrize("nc,nslot,nqb", [(1, 12, 2), (1, 11, 2), (1, 6, 2), (1, 5, 2), (2, 6, 2), (2, 5, 2), (2, 5, 1), (2, 4, 1), (2, 4, 2), (4, 6, 2), (4, 5, 2)])
 @pytest.mark.parametrize("seed", range(40))
 def test_ring_protocol(nc, nslot, nqb, seed):
     """The three roles step by step in a random interleaving, each blocked exactly where the kernel waits.  Loads, products and
