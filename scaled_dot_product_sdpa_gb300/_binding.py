@@ -7,6 +7,7 @@ on a CUDA device, the call raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 import os
@@ -655,11 +656,13 @@ def attn_cache_append(k, v, k_pages, v_pages, table, lengths, counts=None, q=Non
 
 
 def _page_list(x, name):
+    """Address and length of page numbers on the host, and what keeps them there."""
     if not isinstance(x, torch.Tensor):
-        x = torch.tensor(list(x), dtype=torch.int32)
+        x = array.array("i", x if type(x) is list else list(x))
+        return x.buffer_info()[0], len(x), x
     if x.is_cuda or x.dtype != torch.int32 or x.dim() != 1 or not x.is_contiguous():
         raise ValueError(f"gbattn: {name} must be a list of page numbers or a contiguous int32 CPU tensor")
-    return x
+    return x.data_ptr(), x.shape[0], x
 
 
 def attn_cache_copy(k_pages, v_pages, src, dst, stream=None) -> None:
@@ -667,11 +670,10 @@ def attn_cache_copy(k_pages, v_pages, src, dst, stream=None) -> None:
     where a page occurs more than once).  src and dst are page numbers on the host (lists or
     int32 CPU tensors), read before the call returns.  Enqueued on `stream`."""
     dev, _, (_, Hkv, _, d), cache = _cache(k_pages, v_pages)
-    src, dst = _page_list(src, "src"), _page_list(dst, "dst")
-    if src.shape != dst.shape:
+    (src_at, n, src), (dst_at, m, dst) = _page_list(src, "src"), _page_list(dst, "dst")
+    if n != m:
         raise ValueError("gbattn: src and dst must have the same length")
-    _launch("attn_cache_copy", (_lib or load_library()).attn_cache_copy, dev, stream, *cache, Hkv, d, src.data_ptr(),
-            dst.data_ptr(), src.shape[0])
+    _launch("attn_cache_copy", (_lib or load_library()).attn_cache_copy, dev, stream, *cache, Hkv, d, src_at, dst_at, n)
 
 
 def attn_decode_paged_workspace_bytes(Hq: int, Hkv: int, d: int) -> int:

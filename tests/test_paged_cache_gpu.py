@@ -200,6 +200,8 @@ def test_copy_refusals_touch_nothing():
     for src, dst in (([0], [1, 2]), (torch.tensor([0]), torch.tensor([1])), (torch.tensor([0], dtype=torch.int32).cuda(), [1])):
         with pytest.raises(ValueError):
             gb.attn_cache_copy(*view(there), src, dst)
+    with pytest.raises(TypeError):
+        gb.attn_cache_copy(*view(there), [0.5], [1])
     with pytest.raises(gb.GbattnError):
         gb.attn_cache_copy(view(there)[0], view(there)[0], [0], [1])
     assert torch.equal(there.cpu(), store)
