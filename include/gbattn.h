@@ -53,8 +53,9 @@ extern "C" {
 #define GBATTN_ERR_WORKSPACE (-11)  /* attn_fwd_host: device workspace too small             */
 #define GBATTN_ERR_SCRATCH (-12)    /* attn_bwd_noalloc: shape needs more than its fixed buffer */
 #define GBATTN_ERR_DTYPE (-13)      /* dtype is neither GBATTN_F16 nor GBATTN_BF16           */
-#define GBATTN_ERR_STRIDE (-14)     /* a stride is negative or not a multiple of 8 elements,
-                                       or the pages' strides make their rows overlap         */
+#define GBATTN_ERR_STRIDE (-14)     /* a stride is negative, not a multiple of 8 elements or
+                                       reaches beyond 2^40 elements, or the pages' strides
+                                       make their rows overlap                               */
 #define GBATTN_ERR_ROTARY (-15)     /* rotary is not a multiple of 16 in [0, d], or norm
                                        weights or frequencies are incomplete                 */
 #define GBATTN_ERR_PAGES (-16)      /* a page size that is not a multiple of 8, or (copy) a
