@@ -282,6 +282,24 @@ def test_decode_ignores_what_lies_behind_the_last_token(value, d, Hq):
     check_decode(gb.attn_decode_paged(q.cuda(), *view(store.cuda()), table.cuda(), n.cuda(), scale=0.125), ref)
 
 
+@pytest.mark.parametrize("d,G,page", [(64, 1, 8), (64, 12, 24), (64, 20, 16), (128, 2, 24), (128, 12, 8), (128, 20, 136), (256, 1, 8), (256, 20, 24),
+                                      (512, 3, 24), (512, 16, 8)])
+def test_decode_last_tiles_of_every_kind(d, G, page):
+    """Sequences that end anywhere in a group of 16 keys, a page and a tile, with NaN in every slot behind their last token."""
+    lengths, H = [*range(1, 19), 31, 32, 33, 95, 96, 97, 112, 113, *range(126, 131), 143, 144, 145, 255, 256, 257, 0, 400], 2
+    P = sum(-(-m // page) for m in lengths)
+    store, view = cache("slots", P, H, page, d, torch.bfloat16, 81)
+    kp, vp = view(store)
+    table, n = tables(lengths, page, P, 82), torch.tensor(lengths, dtype=torch.int32)
+    for b, m in enumerate(lengths):
+        if m % page:
+            for x in (kp, vp):
+                x[int(table[b, m // page]), :, m % page:] = math.nan
+    q = draw((len(lengths), G * H, d), torch.bfloat16, 83)
+    ref = decode_reference(q, kp, vp, table, n, 1.0 / math.sqrt(d))
+    check_decode(gb.attn_decode_paged(q.cuda(), *view(store.cuda()), table.cuda(), n.cuda()), ref)
+
+
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 def test_decode_peaks_and_tails(dtype):
     """A rising row of logits (the maximum moves in every tile), a single key far above a long flat tail that still counts, and
