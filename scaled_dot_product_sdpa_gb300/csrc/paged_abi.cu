@@ -29,7 +29,7 @@ struct Span {  // bytes [p, p + n)
 
 bool finite_nonneg(float x) { return std::isfinite(x) && x >= 0.f; }
 bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256 || d == 512; }
-// n steps of a stride stay within 2^40 elements, more than any memory, so that no sum of them overflows.
+// n > 0 steps of a stride stay within 2^40 elements, more than any memory, so that no sum of them overflows.
 bool reach_ok(long long s, long long n) { return s >= 0 && s <= (1LL << 40) / n; }
 bool stride_ok(long long s, long long n) { return s % 8 == 0 && s < (1LL << 39) && reach_ok(s, n); }
 bool rows_ok(const Rows &r, int B, int H, int L) {
@@ -269,7 +269,7 @@ extern "C" int attn_cache_append(const void *k, long long k_sb, long long k_sh, 
   if (!k || !v || !k_pages || !v_pages || !table || !lengths || (Hq > 0 && (!q || !q_out))) return GBATTN_ERR_NULL;
   int rc = check_dims(dtype, B, Hq, Hkv, L, d);
   if (rc != GBATTN_OK) return rc;
-  if (table_width <= 0) return GBATTN_ERR_DIMS;
+  if (Hkv <= 0 || table_width <= 0) return GBATTN_ERR_DIMS;
   if (!abi_aligned(k, 16) || !abi_aligned(v, 16) || (Hq > 0 && (!abi_aligned(q, 16) || !abi_aligned(q_out, 16))) ||
       !abi_aligned(table, 4) || !abi_aligned(lengths, 4) || !abi_aligned(counts, 4))
     return GBATTN_ERR_ALIGN;
