@@ -255,7 +255,7 @@ __device__ __forceinline__ void fill_frequencies(Frequencies &f, const RopeParam
 // The tile's cosines and sines: a row of a token's pairs after the other, 16 bytes apart so that
 // neither the threads of fill_turns (neighbouring tokens) nor a row's lanes (neighbouring pairs)
 // meet in few banks.
-__host__ __device__ __forceinline__ int turns_row(int rotary) { return (rotary >> 1) + 2; }
+__host__ __device__ constexpr int turns_row(int rotary) { return (rotary >> 1) + 2; }
 __device__ __forceinline__ void fill_turns(float2 *table, const int *pos, const Frequencies &f, const RopeParams &p) {
   const int shift = 31 - __clz(p.tokens);
   for (int i = threadIdx.x; i < (p.rotary >> 1) << shift; i += kRopeThreads) {
@@ -703,6 +703,23 @@ int plan(RopeParams &p, bool append, int blocks, int at_once) {
 
 size_t turns_bytes(const RopeParams &p) { return p.rotary ? static_cast<size_t>(p.tokens) * turns_row(p.rotary) * sizeof(float2) : 0; }
 
+// Shared memory of a block: the kernels' own arrays (backward: by the elements a lane), and the longest table that
+// plan() can ask for at head_dim d.  Up to 48 KB of both together need no asking.
+constexpr int kOwnBytes = kRopeMaxTokens * (4 + 8) + static_cast<int>(sizeof(Frequencies)) + 1024 * 4;  // rope_kernel, at most
+template <int E>
+constexpr int kBwdOwnBytes = kRopeMaxTokens * 4 + static_cast<int>(sizeof(Frequencies)) + 1024 * 4 + 2 * E * kRopeThreads * 4;
+constexpr int most_turns(int d) {
+  const int rows = kRopeThreads / (d > 256 ? d / 16 : d / 8);
+  return (rows < kRopeMaxTokens ? rows : kRopeMaxTokens) * turns_row(d) * static_cast<int>(sizeof(float2));
+}
+constexpr int kSmemUnasked = 48 * 1024, kSmemSm = 228 * 1024;  // of an SM, 1 KB a block kept by the system
+template <int E>
+constexpr bool fits_unasked(int d) {
+  return kOwnBytes + most_turns(d) <= kSmemUnasked && (E == 16 || kBwdOwnBytes<E> + most_turns(d) <= kSmemUnasked);
+}
+static_assert(fits_unasked<8>(64) && fits_unasked<8>(128) && fits_unasked<8>(256) && fits_unasked<16>(512), "launches without asking");
+static_assert(kBwdResident * (kBwdOwnBytes<16> + most_turns(512) + 1024) <= kSmemSm, "the backward pass at 512");
+
 // The instance for a call's type, norm, layout and head_dim.
 template <bool APPEND>
 auto pick(bool bf, bool norm, bool inter, int d) {
@@ -738,8 +755,14 @@ cudaError_t launch_rope_bwd(RopeLaunch &a) {
   const bool wide = a.p.d > 256;
   const int blocks = a.sm_count * kBwdResident;
   const int grid = plan(a.p, false, std::min(kRopeMaxParts, blocks), wide ? kBwdAtOnce<16> : kBwdAtOnce<8>);
-  const cudaError_t e =
-      launch(pick_bwd(a.bf16, a.interleaved, a.p.d), dim3(grid), kRopeThreads, turns_bytes(a.p), a.stream, RopeParams(a.p));
+  auto *const kern = pick_bwd(a.bf16, a.interleaved, a.p.d);
+  cudaError_t e = cudaSuccess;
+  // Eight tokens of 288 rotated elements and more at 512: up to 55 KB with the kernel's own.  Always asked for as the
+  // most, so that calls of two host threads do not take it from one another.
+  if (wide && kBwdOwnBytes<16> + turns_bytes(a.p) > kSmemUnasked)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most_turns(512));
+  if (e != cudaSuccess) return e;
+  e = launch(kern, dim3(grid), kRopeThreads, turns_bytes(a.p), a.stream, RopeParams(a.p));
   if (e != cudaSuccess) return e;
   return launch(rope_dw_kernel, dim3(a.p.d / 16, a.p.k_w ? 2 : 1), 1024, 0, a.stream, static_cast<const float *>(a.p.parts), grid, a.p.d,
                 a.p.dq_w, a.p.dk_w);
