@@ -9,7 +9,8 @@
 // heads.  The weights P enter the second product as two 16-bit parts, P = hi + lo, in separate
 // columns (N heads are padded to 8 while a product of 128 rows has at least 16 columns, so with
 // up to 8 heads the second part is free); that keeps 16 bits (bf16) or 22 (fp16) of a weight,
-// and they are scaled by 2^13 so that fp16 keeps those of a long tail (2^-38 of the largest).
+// and they are scaled by 2^13 so that fp16 keeps those of a long tail (2^-38 of the largest).  Sums over many tiles leave
+// the tensor cores' accumulators every few tiles (kFold).
 //
 // Work: the (sequence, key head, block of query heads, 128-key tile) units in that order, cut
 // into equal shares, one per persistent CTA, whatever the sequences' lengths.  A share's first
@@ -23,12 +24,14 @@
 // make several TMA boxes per slot; a producer issues one in about 53 cycles, so the boxes are dealt
 // over three of them (one: pages of 8 tokens 645 us, of 16 454, of 128 302; three: 305, 301, 298).
 //
-// Measured on GB300 (64 sequences x 8 key heads x 8000 tokens, d = 128, bf16; 2.1 GB): 296 to 305 us for
+// Measured on GB300 (64 sequences x 8 key heads x 8000 tokens, d = 128, bf16; 2.1 GB): 294 to 303 us for
 // pages of 8 to 128 tokens and up to 8 query heads to a key head, 7.0 TB/s (103% of the copy
-// bandwidth: a read-only stream); 16 query heads 306 to 320.  The same bytes at d = 64 307 to 315 (16
-// heads 400: softmax and both products of 16 columns take longer than a tile of 64 columns does
-// to arrive), d = 256 298 to 307, d = 512 315 to 319 (16 heads 355).  One sequence of 1000 tokens: 9.2 us, the
-// chain of launch, lengths, table, load, two products and the join.
+// bandwidth: a read-only stream); 16 query heads 307 to 315.  The same bytes at d = 64 310 to 317 (16
+// heads 382: softmax and both products of 16 columns take longer than a tile of 64 columns does
+// to arrive), d = 256 298 to 308, d = 512 317 to 320.  More heads to a key head: 17 to 32 of 128 take 482 to 541,
+// 32 of 64 934, of 256 449 (a tile's softmax of 32 columns); blocks beyond 32 heads (16 at d = 512) read the cache again: 64 heads
+// 1052 (d = 512: 1235), 128 2072 (2431).  One sequence of 1000 tokens: 9.2 us, the chain of launch, lengths, table, load, two products
+// and the join.  No instance spills but 16 heads at d = 64 (68 bytes, two CTAs of 128 registers a thread).
 #include <atomic>
 
 #include "paged_decode.cuh"
@@ -45,6 +48,13 @@ constexpr int kAhead = 4;      // tiles whose page numbers a producer reads ahea
 constexpr int kThreads = 160 + 32 * kProducers;
 constexpr float kShift = 13.f;  // weights are kept times 2^13
 constexpr float kSlack = 2.f;   // the running maximum moves when a logit exceeds it by 2^2
+// The tensor cores add to an fp32 accumulator by cutting off what falls below its last bit, so that a sum over n products
+// of 16 keys comes out too small by about n 2^-24 (512 tiles of values of 1 in fp16: 3837 x 2^-24).  So O is begun anew
+// every kFold tiles, and whenever the running maximum moves; what the tiles before add up to is kept, rounded to nearest
+// and scaled to the maximum, in columns of its own.  With 8 that error stays at 2^-18 however long a row is.  GB300, 64 x 8
+// key heads x 8000 keys x 128, and the same bytes at d = 64: with up to 8 query heads all choices 311 us and 322; 16 heads
+// at d = 64: every 4 tiles 398, 8 386, 16 379, never 377; 32 heads at 128: 576, 541, 530, 527.
+constexpr int kFold = 8;
 
 template <int D, int NH>
 struct PagedCfg {
@@ -87,7 +97,8 @@ struct PagedCfg {
   static_assert(SMEM_BYTES <= SMEM_MOST, "shared memory budget");
   static constexpr int NO = D <= 128 ? 1 : D / 128;     // 128-column blocks of O
   static constexpr int T_O = 2 * NQ;                    // TMEM columns: S twice, then O twice
-  static constexpr int T_USED = T_O + 2 * NO * NP;       // O of two segments
+  static constexpr int T_SUM = T_O + 2 * NO * NP;        // O of two segments, then the sums of the tiles before O was last begun
+  static constexpr int T_USED = T_SUM + NO * NH;
   static constexpr int T_COLS = T_USED <= 64 ? 64 : T_USED <= 128 ? 128 : T_USED <= 256 ? 256 : 512;
   static_assert(T_USED <= 512, "tensor memory");
 };
@@ -111,7 +122,8 @@ __device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t (&r)[N]) {
 }
 template <int N>
 __device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t (&r)[N]) {
-  if constexpr (N == 16) tmem_st32x16(a, r);
+  if constexpr (N == 8) tmem_st32x8(a, r);
+  else if constexpr (N == 16) tmem_st32x16(a, r);
   else if constexpr (N == 32) tmem_st32x32(a, r);
   else tmem_st32x64(a, r);
 }
@@ -287,6 +299,7 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, NH>::RES)
     Start start;
     uint32_t tmem_base;
     volatile uint32_t abort_flag;
+    volatile uint32_t fresh[2];  // whether a tile's PV begins O anew, by the buffer of its weights
   };
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -534,9 +547,10 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, NH>::RES)
           if (last) umma_commit(BAR(C::B_QEMPTY + qb));
         }
       };
-      auto pv = [&](uint32_t i, uint32_t seg, bool first, int groups) {  // groups of 16 keys
+      auto pv = [&](uint32_t i, uint32_t seg, int groups) {  // groups of 16 keys
         const uint32_t buf = i & 1u, o = tmem + C::T_O + (seg & 1u) * (C::NO * C::NP);
         wait(C::B_PFULL + buf, i >> 1);
+        const bool first = misc.fresh[buf] != 0;
         for (int c = 0; c < C::NC / C::VS; ++c) {
           wait(C::B_FULL + slot, lap);
           if (C::VS == 2) wait(C::B_FULL + slot + 1, lap);
@@ -559,21 +573,20 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, NH>::RES)
       Walk<false> w(p, start);
       Seg s;
       uint32_t i = 0, seg = 0;
-      bool pending = false, pending_first = false;  // PV(i - 1) is due
+      bool pending = false;  // PV(i - 1) is due
       uint32_t pending_seg = 0;
       int pending_groups = 0;
       while (got && w.next(s)) {
         for (int j = 0; got && j < s.count; ++j, ++i) {
           qk(i, seg, j == 0, j == s.count - 1);
-          if (got && pending) pv(i - 1, pending_seg, pending_first, pending_groups);
+          if (got && pending) pv(i - 1, pending_seg, pending_groups);
           pending = true;
-          pending_first = j == 0;
           pending_seg = seg;
           pending_groups = (min(kPagedTile, s.len - (s.tile + j) * kPagedTile) + 15) >> 4;
         }
         ++seg;
       }
-      if (got && pending) pv(i - 1, pending_seg, pending_first, pending_groups);
+      if (got && pending) pv(i - 1, pending_seg, pending_groups);
       if (misc.abort_flag) {  // after a time-out: products in flight end before the CTA does
         umma_commit(BAR(C::B_DRAIN));
         wait_drain(BAR(C::B_DRAIN), 0, p.wait_limit);
@@ -609,10 +622,13 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, NH>::RES)
       else
         wait(C::B_PDONE + static_cast<int>(t & 1), t >> 1);
     };
-    // A segment's results wait for its last PV; they are taken after the next segment's first tile.
+    constexpr int W = NH < 32 ? 8 : 16;  // columns at once (8 and 16: 16 heads at d = 64 387 and 395 us, 32 at 128 572 and 541)
+    const uint32_t sum_at = lanes + C::T_SUM;
+    // A segment's results wait for its last PV; they are taken after the next segment's first tile (and so before
+    // sum_at holds sums of that one).
     struct {
       int heads = 0;  // 0: none due
-      bool whole, begins;
+      bool whole, begins, sums;  // sums: there are some in sum_at
       uint32_t last, seg;
       size_t row0;
     } due;
@@ -648,7 +664,18 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, NH>::RES)
         const int col = ob * 128 + tid;
         if (!ok || (D < 128 && tid >= D)) continue;
 #pragma unroll
-        for (int h = 0; h < NH; ++h) o[h] = __float_as_uint((__uint_as_float(o[h]) + __uint_as_float(o[NH + h])) * inv[h]);
+        for (int h = 0; h < NH; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) + __uint_as_float(o[NH + h]));
+        if (due.sums) {
+#pragma unroll
+          for (int g = 0; g < NH; g += W) {
+            uint32_t t[W];
+            tmem_ld<W>(sum_at + ob * NH + g, t);
+#pragma unroll
+            for (int h = 0; h < W; ++h) o[g + h] = __float_as_uint(__uint_as_float(t[h]) + __uint_as_float(o[g + h]));
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < NH; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * inv[h]);
         if (!due.whole) {
           float *to = p.part_o + part * NH * D + col;
 #pragma unroll
@@ -680,7 +707,9 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, NH>::RES)
         m[h] = -INFINITY;
         l[h] = 0.f;
       }
-      for (int j = 0; j < s.count; ++j, ++i) {
+      int since = 0;      // tiles in O
+      bool sums = false;  // whether sum_at holds those before them
+      for (int j = 0; j < s.count; ++j, ++i, ++since) {
         // After a time-out the remaining tiles run through the barriers only.
         const int buf = static_cast<int>(i & 1), n = s.len - (s.tile + j) * kPagedTile;
         uint32_t x[NH];
@@ -708,7 +737,6 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, NH>::RES)
         }
         softmax_sync();
         // ---- the running maximum, and what it does to the sums and to O
-        float keep[NH];
         int moved = 0;  // the same in every thread
 #pragma unroll
         for (int g = 0; g < NH; g += 4)
@@ -726,7 +754,13 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, NH>::RES)
           moved = 0;
 #pragma unroll
           for (int h = 0; h < NH; ++h) m[h] = top[h];
-        } else if (moved) {
+        }
+        if (i >= 2) wait_pv(i - 2);  // the weights' buffer, and fresh, are free again
+        const bool begins = j == 0 || moved || since == kFold;  // O anew
+        if (begins && j > 0) {
+          // Before the weights, not after: the factors need not live beside them (16 heads at d = 64 387 us, after them 458;
+          // 32 at 128 541 and 605).
+          float keep[NH];
 #pragma unroll
           for (int h = 0; h < NH; ++h) {
             const bool up = top[h] > m[h] + kSlack;
@@ -734,9 +768,32 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, NH>::RES)
             l[h] *= keep[h];
             m[h] = up ? top[h] : m[h];
           }
+          wait_pv(i - 1);
+          if (ok) {
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < C::NO * NH; c += W) {
+              const uint32_t from = o_at + c / NH * C::NP + c % NH;
+              uint32_t t[W], o[W];
+              tmem_ld<W>(from, t);
+              tmem_ld<W>(from + NH, o);
+#pragma unroll
+              for (int h = 0; h < W; ++h) t[h] = __float_as_uint(__uint_as_float(t[h]) + __uint_as_float(o[h]));
+              if (sums) {
+                tmem_ld<W>(sum_at + c, o);
+#pragma unroll
+                for (int h = 0; h < W; ++h) t[h] = __float_as_uint(__uint_as_float(t[h]) + __uint_as_float(o[h]));
+              }
+#pragma unroll
+              for (int h = 0; h < W; ++h) t[h] = __float_as_uint(__uint_as_float(t[h]) * keep[c % NH + h]);
+              tmem_st<W>(sum_at + c, t);
+            }
+          }
+          sums = true;
+          since = 0;
         }
+        if (tid == 0) misc.fresh[buf] = begins;
         // ---- the weights of this thread's key, as hi + lo
-        if (i >= 2) wait_pv(i - 2);
         const uint32_t prow = base + C::OFF_P + buf * C::P_BYTES + tid * (4 * NH);
         const uint32_t swz = NH == 8 ? (tid >> 2) & 1 : NH == 16 ? (tid >> 1) & 3 : tid & 7;
 #pragma unroll
@@ -761,23 +818,6 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, NH>::RES)
             st_shared_v4(prow + (((g >> 3) ^ swz) << 4), hi[0], hi[1], hi[2], hi[3]);
             st_shared_v4(prow + ((((NH + g) >> 3) ^ swz) << 4), lo[0], lo[1], lo[2], lo[3]);
           }
-        if (moved) {
-          wait_pv(i - 1);
-          if (ok) {
-            tc_fence_after();
-#pragma unroll
-            for (int ob = 0; ob < C::NO; ++ob) {
-              uint32_t o[C::NP];
-              tmem_ld<C::NP>(o_at + ob * C::NP, o);
-#pragma unroll
-              for (int h = 0; h < NH; ++h) {
-                o[h] = __float_as_uint(__uint_as_float(o[h]) * keep[h]);
-                o[NH + h] = __float_as_uint(__uint_as_float(o[NH + h]) * keep[h]);
-              }
-              tmem_st<C::NP>(o_at + ob * C::NP, o);
-            }
-          }
-        }
         if ((n & 15) != 0 && n < kPagedTile) {
           // PV takes keys in groups of 16 (all 128, and every row behind the last token cleared by its own
           // thread: 154 x 32 heads of 4 tokens x 128 82.8 us, now 56.9).  Whatever lies behind the last token in its group (unwritten
@@ -816,6 +856,7 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, NH>::RES)
       due.heads = heads;
       due.whole = s.count == s.tiles;
       due.begins = s.tile == 0;
+      due.sums = sums;
       due.last = i - 1;
       due.seg = seg;
       due.row0 = static_cast<size_t>(s.b) * p.Hq + kv * p.G + block * NH;
