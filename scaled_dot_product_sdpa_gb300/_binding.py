@@ -362,11 +362,13 @@ def attn_fwd_host(q, k, v, causal: bool = False, scale: float | None = None, o=N
 # belongs to the stream that it runs on.  A decoding step makes several of these calls, each
 # worth a few microseconds on the GPU, so the checks read each property of a tensor once.
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
-_current_stream = torch._C._cuda_getCurrentRawStream  # of a device index; torch.cuda.current_stream costs 3 us
-_current_device = torch._C._cuda_getDevice
+# Private names of torch, each with the public way beside it (a torch without CUDA lacks them).
+# Of a device index; torch.cuda.current_stream costs 3 us.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 # torch.empty without its argument parser, on the current device (0.9 us a tensor instead of 1.5, and more between
-# launches: attn_decode_paged 22.0 us a call, with this 18.8, attn_rope 16.7 and 13.4); None where torch lacks it.
-_empty_strided = getattr(getattr(torch._C, "_dynamo", None) and torch._C._dynamo.guards, "_empty_strided_cuda", None)
+# launches: attn_decode_paged 22.0 us a call, with this 18.8, attn_rope 16.7 and 13.4); None: torch.empty.
+_empty_strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
 
 
 def _empty(shape, dtype, like, stream):

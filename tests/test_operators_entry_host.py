@@ -25,3 +25,16 @@ def test_append_without_key_heads_is_refused(heads):
               f"for more in (dict(), dict(wq=None, wk=None), dict(wq=None, wk=None, q=None, qo=None, Hq=0)):\n"
               f"    print(t.append(lib, Hkv={heads}, **more) == t.code('DIMS'))\n")
     assert out.split() == ["True"] * 3, out
+
+
+@pytest.mark.parametrize("lacks", ["torch._C._cuda_getCurrentRawStream torch._C._cuda_getDevice", "torch._C._dynamo", "torch._C._dynamo.guards",
+                                   "torch._C._dynamo.guards._empty_strided_cuda"])
+def test_the_package_is_imported_without_torch_s_private_names(lacks):
+    """A torch without CUDA, or with other private names: the package is imported, and a call says what it needs."""
+    drop = "".join(f"if hasattr({n.rpartition('.')[0]}, '{n.rpartition('.')[2]}'): del {n}\n" for n in lacks.split())
+    out = run(f"import torch\n{drop}"
+              "import scaled_dot_product_sdpa_gb300 as gb\n"
+              "q = torch.zeros(1, 2, 3, 64, dtype=torch.float16)\n"
+              "try:\n    gb.attn_rope(q, None, None)\nexcept ValueError as e:\n    print(e)\n"
+              "print(gb.attn_rope_frequencies(64, device='cpu')[0].shape[0])\n")
+    assert "must be on a CUDA device" in out and out.split()[-1] == "32", out
