@@ -18,8 +18,8 @@ constexpr int kThreads = 256, kVecs = 4;
 template <int N>
 struct CopyParams {
   CopyShape s;
-  int n, blocks;  // blocks per page
-  int src[N], dst[N];
+  int blocks;  // per page
+  int src[N], dst[N];  // read as far as the grid's pairs go
 };
 
 template <int N>
@@ -58,12 +58,9 @@ template <int N>
 cudaError_t launch_n(const CopyLaunch &a) {
   CopyParams<N> p;
   p.s = a.s;
-  p.n = a.n;
   p.blocks = (a.s.pieces * a.s.piece_vecs + kThreads * kVecs - 1) / (kThreads * kVecs);
   std::memcpy(p.src, a.src, sizeof(int) * a.n);
   std::memcpy(p.dst, a.dst, sizeof(int) * a.n);
-  std::memset(p.src + a.n, 0, sizeof(int) * (N - a.n));
-  std::memset(p.dst + a.n, 0, sizeof(int) * (N - a.n));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * a.n) * static_cast<unsigned>(p.blocks));
   cfg.blockDim = dim3(kThreads);

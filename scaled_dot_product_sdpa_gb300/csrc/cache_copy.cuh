@@ -6,7 +6,8 @@
 namespace gbattn {
 
 // Pages of one launch.  The pairs travel as kernel arguments (host lists, no copy to the
-// device); their room is 32,764 bytes in all.
+// device), whose room is 32,764 bytes in all: the larger list is the round number below
+// (32,764 - sizeof(CopyShape) - 4) / 8, the smaller one keeps short calls' arguments to 0.5 KB.
 constexpr int kCopyPairsSmall = 60;
 constexpr int kCopyPairsLarge = 4000;
 
