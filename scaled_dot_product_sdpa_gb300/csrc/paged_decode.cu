@@ -971,8 +971,9 @@ cudaError_t launch_paged(const PagedLaunch &a) {
     if (e != cudaSuccess) return e;
     if (dev < 64) configured |= 1ull << dev;
   }
-  // At most one CTA per unit of work that the tables have room for.
-  const long long row_tiles = (static_cast<long long>(a.p.table_w) * a.p.page + kPagedTile - 1) / kPagedTile;
+  // At most one CTA per unit of work that the tables have room for (and lengths, of 31 bits, can name).
+  const long long row_tiles =
+      std::min((static_cast<long long>(a.p.table_w) * a.p.page + kPagedTile - 1) / kPagedTile, (1LL << 31) / kPagedTile);
   const long long units = static_cast<long long>(a.p.B) * a.p.Hkv * a.p.blocks * row_tiles;
   const unsigned grid = static_cast<unsigned>(std::min<long long>(units, std::min(C::RES * a.sm_count, kPagedMaxCtas)));
   cudaLaunchConfig_t cfg = {};

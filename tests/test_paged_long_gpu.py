@@ -82,3 +82,19 @@ def test_rising_rows_of_many_tiles(dtype, d, G):
     v = (1 + 0.1 * torch.randn(tiles * 128, d, generator=torch.Generator().manual_seed(6))).to(dtype)
     lengths = torch.tensor([5760, 5759, 5633, 5400, 1025, 1024, 2049, 1153], dtype=torch.int32)
     check_rows(dtype, d, G, k.to(dtype), v, q.to(dtype), torch.arange(tiles, dtype=torch.int32), lengths)
+
+
+def test_tables_with_room_for_more_than_lengths_can_say():
+    """65536 sequences, each with a table of 2^30 pages of 2^24 tokens: the units of work that they have room for pass 2^63."""
+    N, d, page, n = 65536, 64, 1 << 24, 300
+    kp, vp = (torch.zeros(1, 1, page, d, dtype=torch.float16, device="cuda") for _ in range(2))
+    kp[0, 0, :n], vp[0, 0, :n] = (quantised((2, n, d), 7, 8) + torch.tensor([0.0, 1.0])[:, None, None]).half().cuda()
+    q = quantised((1, 1, d), 8, 8).half().cuda()
+    table = torch.zeros(1, 1 << 30, dtype=torch.int32, device="cuda")
+    lengths = torch.zeros(N, dtype=torch.int32, device="cuda")
+    lengths[[0, 777, N - 1]] = n
+    o, lse = gb.attn_decode_paged(q.expand(N, 1, d), kp, vp, table.expand(N, -1), lengths)
+    want = gb.attn_decode_paged(q, kp, vp, table[:, :1], lengths[:1])
+    at = lengths > 0
+    assert torch.isfinite(want[1]).all() and torch.equal(o[at], want[0].expand(3, 1, d)) and torch.equal(lse[at], want[1].expand(3, 1))
+    assert (o[~at] == 0).all() and torch.isneginf(lse[~at]).all()
