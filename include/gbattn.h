@@ -377,6 +377,11 @@ int attn_cache_copy(void *k_pages, void *v_pages, long long page_stride, long lo
  *                that can run at the same time need one each.
  *   Hq         : a multiple of Hkv (else GBATTN_ERR_HEADS).  scale: finite, > 0.
  * What lies behind a sequence's last token in its last page does not matter (NaN included).
+ * Arithmetic: logits, maxima and sums in fp32; the products of weights and values run on the tensor
+ * cores with each weight as the sum of two values of the cache's type, so with 22 of its bits in
+ * fp16 and 16 in bf16 (2^-17 of it at most); their sums are rounded to fp32 every 1024 tokens, so
+ * that no error grows with the length; one rounding to the output's type.  The same call gives
+ * the same bits.
  */
 int attn_decode_paged(const void *q, long long q_sb, long long q_sh, const void *k_pages, const void *v_pages,
                       long long page_stride, long long head_stride, long long slot_stride, int pages, int page,

@@ -691,7 +691,8 @@ def attn_decode_paged(q, k_pages, v_pages, table, lengths, scale: float | None =
     """Decode over a paged cache: O [B, Hq, d] and LSE [B, Hq] for one query row q ([B, Hq, d] or
     [B, Hq, 1, d]) per sequence and head against the lengths[b] tokens that table (int32
     [B, width]) finds in k_pages, v_pages [pages, Hkv, page, d]; Hq a multiple of Hkv.  An empty
-    sequence gives zeros and -inf.  Outputs, and the workspace unless given (a contiguous CUDA
+    sequence gives zeros and -inf.  Sums in float32; the weights that meet the values keep 22 bits
+    with float16 and 16 with bfloat16.  Outputs, and the workspace unless given (a contiguous CUDA
     tensor of attn_decode_paged_workspace_bytes bytes), are allocated by torch.  Enqueued on
     `stream`."""
     dev, code, (_, Hkv, _, d), cache = _cache(k_pages, v_pages)

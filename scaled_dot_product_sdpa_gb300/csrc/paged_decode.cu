@@ -820,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, NH>::RES)
           }
         if ((n & 15) != 0 && n < kPagedTile) {
           // PV takes keys in groups of 16 (all 128, and every row behind the last token cleared by its own
-          // thread: 154 x 32 heads of 4 tokens x 128 82.8 us, now 56.9).  Whatever lies behind the last token in its group (unwritten
+          // thread: 154 x 32 heads of 4 tokens x 128 82.8 us, now 52).  Whatever lies behind the last token in its group (unwritten
           // slots, earlier tiles) times a weight of zero must be zero: clear those rows of V, eight
           // threads to a row.
           if constexpr (C::NSLOT < 3 * C::NC) {

@@ -17,9 +17,9 @@ namespace gbattn {
 // Persistent CTAs on an SM.  Two where registers and shared memory hold them (up to 8 heads at once
 // and d <= 128, or 16 and d = 64): one CTA's tile is a chain of a softmax and two products, and at
 // d = 64 or with short sequences the second fills its gaps.  GB300, one and two CTAs: 128 x 8 heads x
-// 8000 keys x 64 363 and 313 us, 64 of them with 16 query heads a key head 257 and 212; 256 sequences
-// of 100 keys x 128, 32/8 heads, 38.2 and 31.4; long rows at d = 128 303 and 301; a single sequence
-// loses (1000 keys, 8 heads x 128, 9.05 and 9.20; 20000 keys x 64, 128/8 heads, 21.8 and 23.4).
+// 8000 keys x 64 394 and 319 us, 64 of them with 16 query heads a key head 251 and 201; 256 sequences
+// of 100 keys x 128, 32/8 heads, 33.9 and 30.2; 154 x 32 heads of 4 keys 70.4 and 52.0; long rows at
+// d = 128 315 and 309; one sequence of 1000 keys 9.5 and 9.5, of 20000 x 64, 128/8 heads, 21.1 and 19.7.
 constexpr int paged_resident(int d, int heads) { return (heads == 8 && d <= 128) || (heads == 16 && d == 64) ? 2 : 1; }
 constexpr int kPagedMaxCtas = 304;  // CTAs at most (two on each SM); sizes the workspace
 constexpr int kPagedTile = 128;     // keys per tile

@@ -20,9 +20,12 @@
 // Measured on GB300: rotation of 8 x 64 x 512 x 128 in fp16 25.3 us (5.3 TB/s), of half of each head of
 // 100003 x 32 x 64 134 us (6.1 TB/s); norm and rotation of 4 x 40 x 2048 x 128 in bf16 34.9 us (4.8 TB/s), its
 // backward pass 57.5 (4.4 TB/s); the append of 8 x 48 x 1024 x 128 37.9, with norms 41.2 (5.3, 4.9 TB/s).
-// What bounds the norms is issue (57% of the slots, 127 instructions for a warp's two rows of
-// 128) and the chain of loads, reduction and stores at 24 warps an SM.  Tried and slower or flat: 16
-// elements a lane without pairs (44.5 and 92 us), addresses worked out per unit (36.6, 62.3), the
+// With norms neither HBM (44% of its peak rate; 50% backward) nor issue (57% and 54% of the slots) is at its
+// limit: a unit is a chain of loads, a reduction and stores, and 24 (16) warps an SM are what the registers leave to
+// overlap them.  Few heads leave a thread's rows empty and share a tile's angles among few rows: one head each
+// of queries and keys x 40495 x 512 84.2 us (29% of the copy bandwidth; backward 113, 32%), the backward pass of two
+// heads each x 25 x 8169 x 64 105 (44%).  Tried and slower or flat: 16 elements a lane without the fp32 pairs
+// (44.5 and 92 us; with them only at d = 512), addresses worked out per unit (36.6, 62.3), the
 // next unit's loads ahead in registers (39 to 60) or through shared memory by asynchronous copies, two to
 // four units deep (38.4, 62 to 72), smaller shares in two or four waves (36.9 and more).
 //
@@ -45,7 +48,8 @@ namespace {
 // rotation of 8 x 64 x 512 x 128 25.3 us, 33.0; with norms of 4 x 40 x 2048 x 128 34.9, 48.5.  The
 // backward pass reads twice as much a row: 4 rows and 2 blocks 57.5 us, 3 and 2 61.1, 2 and 3 77.7.
 // With 16 elements a lane (8 x 32 x 106 x 512, and one head of 40495 rows): 2 rows and 2 blocks 32.8 and
-// 113 us, 2 and 1 32.2 and 143, 1 and 2 33.5 and 99.5.
+// 113 us, 2 and 1 32.2 and 143, 1 and 2 33.5 and 99.5.  Those instances of the backward pass are the only ones that
+// spill (64 to 76 bytes a thread, at 128 registers); 8 x 40 x 304 x 512 turned as a whole 72.0 us (61%).
 template <int E>
 constexpr int kAtOnce = E == 8 ? 4 : 2;
 template <int E>
