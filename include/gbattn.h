@@ -460,7 +460,8 @@ int attn_cache_keep(void *k_pages, void *v_pages, long long page_stride, long lo
  *                the same time need one each.
  *   Hq         : a multiple of Hkv (else GBATTN_ERR_HEADS).  scale: finite, > 0.
  * Keys of tokens that a row does not see may hold anything; values within a sequence's length
- * are finite (a weight of zero times an infinity or NaN is NaN, for every row of that sequence).
+ * are finite (a weight of zero times an infinity or NaN is NaN, for every row of that sequence): up to
+ * the largest of their type, whatever their signs.  In bf16 those below 2^-77 lose bits, below 2^-86 they may count as zero.
  * What lies behind the last token in its page does not matter.
  * Arithmetic: logits, maxima and sums in fp32.  Where a key head has up to 32 rows (Hq / Hkv * T) each weight
  * enters its product with the values as the sum of two values of the cache's type, as in

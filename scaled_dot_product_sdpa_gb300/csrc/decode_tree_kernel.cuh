@@ -4,7 +4,7 @@
 // Both products run on the tensor cores with the rows (a key head's query heads times new tokens) as
 // the 128-row operand, so that a softmax thread owns one row and no maximum or sum leaves it:
 //     S [128 rows x 128 keys] = Q K^T,   O [128 rows x d] += P V,   P from tensor memory, over its S.
-// Weights enter the second product (in fp16 times 2^11, see kShift) of up to 32 rows as two 16-bit parts, P = hi + lo,
+// Weights enter the second product (in fp16 times 2^11, in bf16 times 2^-40, see kShift) of up to 32 rows as two 16-bit parts, P = hi + lo,
 // over twice the keys (that keeps 16 bits in bf16, 22 in fp16), of more rows rounded to the cache's type (see
 // tree_split_weights).  The tensor cores add to an fp32 accumulator by cutting off what falls below its last bit, about 2^-24
 // of a sum a product: so a sum leaves its accumulator every `fold` tiles (2^-15 to 2^-14 in fp16, 2^-12 to 2^-11 in bf16, an
@@ -49,9 +49,15 @@ namespace {
 constexpr unsigned kTreeSmemAlign = 7;  // GBATTN_DEV_SMEM_ALIGN
 constexpr int kProducers = 3;
 constexpr int kAhead = 2;       // tiles whose page numbers a producer reads ahead
-// Weights are kept times 2^11 in fp16, so that those of a long tail stay normal numbers; bf16 has the range of fp32.
+// Weights are kept times 2^11 in fp16, so that those of a long tail stay normal numbers.  In bf16, whose values reach the end of
+// fp32, they enter the second product times 2^-40: 2^31 of them, of up to 2^4, times the largest value stay below 2^128.  (By a
+// product of its own, which is exact: off the exponent's argument it would round the weights to 2^-19 of themselves.)
 template <bool BF>
 constexpr float kShift = BF ? 0.f : 11.f;
+template <bool BF>
+constexpr float kValueScale = BF ? 0x1p-40f : 1.f;
+template <bool BF>
+constexpr float kValueBack = BF ? 0x1p40f : 1.f;
 constexpr int kTreeSegs = 8;    // segments whose words are kept
 constexpr float kSlack = 4.f;   // the running maximum moves when a logit exceeds it by 2^4
 
@@ -230,6 +236,11 @@ __device__ __forceinline__ float max32(const uint32_t (&r)[32]) {
     m[k] = fmaxf(fmax3(fmax3(s[8 * k], s[8 * k + 1], s[8 * k + 2]), s[8 * k + 3], s[8 * k + 4]), fmax3(s[8 * k + 5], s[8 * k + 6], s[8 * k + 7]));
   return fmax3(m[0], m[1], fmaxf(m[2], m[3]));
 }
+// Two weights as they enter the second product.
+template <bool BF>
+__device__ __forceinline__ uint64_t scaled(uint64_t w) {
+  return BF ? fmul2(w, f32x2(kValueScale<BF>, kValueScale<BF>)) : w;
+}
 // 16 logits as weights 2^(s c2 - m), rounded once; adds the weights to acc.
 template <bool BF>
 __device__ __forceinline__ void pack16(const uint32_t (&r)[16], uint32_t *w, uint64_t c2x2, uint64_t negm, uint64_t (&acc)[4], float &top) {
@@ -241,7 +252,8 @@ __device__ __forceinline__ void pack16(const uint32_t (&r)[16], uint32_t *w, uin
     f32x2_split(ffma2(f32x2(s[2 * c], s[2 * c + 1]), c2x2, negm), x0, x1);
     const float w0 = ex2_approx(x0), w1 = ex2_approx(x1);
     acc[c & 3] = fadd2(acc[c & 3], f32x2(w0, w1));
-    w[c] = pack2<BF>(w0, w1);
+    f32x2_split(scaled<BF>(f32x2(w0, w1)), x0, x1);
+    w[c] = pack2<BF>(x0, x1);
   }
 }
 // 32 logits as weights 2^(s c2 - m): hi parts, then lo parts, 16 columns each, over the logits at `to`.  Adds the weights to acc.
@@ -255,10 +267,11 @@ __device__ __forceinline__ void weights32(const uint32_t (&r)[32], uint32_t to, 
     f32x2_split(ffma2(f32x2(s[2 * c], s[2 * c + 1]), c2x2, negm), x0, x1);
     const float w0 = ex2_approx(x0), w1 = ex2_approx(x1);
     acc[c & 3] = fadd2(acc[c & 3], f32x2(w0, w1));
+    f32x2_split(scaled<BF>(f32x2(w0, w1)), x0, x1);
     if constexpr (LO)
-      split_weights<BF>(w0, w1, w[c], w[16 + c]);
+      split_weights<BF>(x0, x1, w[c], w[16 + c]);
     else
-      w[c] = pack2<BF>(w0, w1);
+      w[c] = pack2<BF>(x0, x1);
   }
   if constexpr (LO)
     tmem_st32x32_async(to, w);
@@ -963,7 +976,7 @@ __global__ void __launch_bounds__(TreeCfg<D, RT>::THREADS, 1)
       }
       if (any) {
         const float lse2 = m - kShift<BF> + __log2f(l);
-        const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
+        const float inv = l == 0.f ? 0.f : __fdividef(kValueBack<BF>, l);
         if (valid && ok && half == 0 && (C::WG == 1 || RT == 2 || stream == 0) && whole) p.lse[row_out] = lse2 * 0.69314718055994531f;
         if (valid && ok && (C::WG == 1 || RT == 2 || stream == 0) && !whole) p.part_lse[(part * RT + row_tile) * p.s.rows + r] = lse2;
         const int c0 = C::WG == 2 && RT == 1 ? stream * (C::DV / 2) : 0, c1 = C::WG == 2 && RT == 1 ? c0 + C::DV / 2 : C::DV;
@@ -1016,6 +1029,8 @@ __global__ void __launch_bounds__(TreeCfg<D, RT>::THREADS, 1)
 }
 
 constexpr int kJoinThreads = 256, kJoinAtOnce = 8;
+constexpr float kJoinScale = 0x1p-8f;  // up to kTreeMaxCtas values of the largest size add up to one within fp32
+static_assert(kTreeMaxCtas * kJoinScale < 1.f, "sums of a join");
 
 // Joins the units that were cut: block (c, y, z) takes 64 columns and 32 rows (row tiles one after the other) of the unit that CTA
 // c's share ends in, a warp eight of the columns, a lane a row; the loads of kJoinAtOnce parts are under way together.
@@ -1067,12 +1082,12 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
       if (first + u < rec.parts) {
         const float v[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = fmaf(w, v[e], o[e]);
+        for (int e = 0; e < 8; ++e) o[e] = fmaf(w * kJoinScale, v[e], o[e]);
       }
     }
   }
   if (c == 0 && half == 0) p.lse[out] = (M + __log2f(sum)) * 0.69314718055994531f;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const float inv = sum == 0.f ? 0.f : 1.f / (sum * kJoinScale);
   uint32_t h[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) h[e] = pack2<BF>(o[2 * e] * inv, o[2 * e + 1] * inv);
