@@ -9,7 +9,8 @@
 // tree_split_weights).  The tensor cores add to an fp32 accumulator by cutting off what falls below its last bit, about 2^-24
 // of a sum a product: so a sum leaves its accumulator every `fold` tiles (2^-15 to 2^-14 in fp16, 2^-12 to 2^-11 in bf16, an
 // eighth to a quarter of the result's half step), for a place in the workspace where it is added to in fp32, rounded to
-// nearest, and the weights' sum with it.
+// nearest, and the weights' sum with it.  Each such run of tiles goes by its own maximum, so that a weight's last bit is one of that
+// run's, however long the row is (in fp16 weights below 2^-25 of the maximum are subnormal, kept to 2^-36 of it).
 //
 // d <= 128: two accumulator sets ("streams"), each an S tile, an O tile and a softmax warpgroup of its own,
 // so that one's products run while the other's softmax does.  Where a key head's rows fill one row tile
@@ -821,7 +822,8 @@ __global__ void __launch_bounds__(TreeCfg<D, RT>::THREADS, 1)
                 tc_fence_after();
               }
               if (fold && ok) {
-                const float keep = folded && m != -INFINITY ? ex2_approx(m_sums - m) : 0.f;
+                // (Two maxima of -inf: sums of nothing, whatever their factors; fminf drops their difference, a NaN.)
+                const float keep = ex2_approx(fminf(m_sums - m, 0.f)), add = ex2_approx(fminf(m - m_sums, 0.f));
 #pragma unroll 1
                 for (int c = 0; c < C::DV; c += 32) {
                   uint32_t o[32];
@@ -829,7 +831,7 @@ __global__ void __launch_bounds__(TreeCfg<D, RT>::THREADS, 1)
                   if (valid)
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
-                      float4 x = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+                      float4 x = make_float4(__uint_as_float(o[e]) * add, __uint_as_float(o[e + 1]) * add, __uint_as_float(o[e + 2]) * add, __uint_as_float(o[e + 3]) * add);
                       if (folded) {
                         const float4 y = sums[(c + e) / 4 * p.s.rows];
                         x = make_float4(fmaf(y.x, keep, x.x), fmaf(y.y, keep, x.y), fmaf(y.z, keep, x.z), fmaf(y.w, keep, x.w));
@@ -837,9 +839,10 @@ __global__ void __launch_bounds__(TreeCfg<D, RT>::THREADS, 1)
                       sums[(c + e) / 4 * p.s.rows] = x;
                     }
                 }
-                l_sums = fmaf(l_sums, keep, l);  // (the weights' sum, too: in one number each tile of a row of 2^31 would be rounded to 2^-8)
+                l_sums = fmaf(l_sums, keep, l * add);  // (the weights' sum, too: in one number each tile of a row of 2^31 would be rounded to 2^-8)
                 l = 0.f;
-                m_sums = m;
+                m_sums = fmaxf(m_sums, m);
+                m = top;  // the next `fold` tiles go by their own maximum
                 folded = true;
               }
               const bool up = top > m + kSlack;
@@ -918,8 +921,14 @@ __global__ void __launch_bounds__(TreeCfg<D, RT>::THREADS, 1)
         if (lane == 0) mbar_arrive(BAR(C::B_PFULL + buf));
       }
       // ---------------------------------------------------------- the segment's results
-      const float back = folded && m != -INFINITY ? ex2_approx(m_sums - m) : 0.f;  // of what left the accumulator
-      if (folded) l = fmaf(l_sums, back, l);
+      // What left the accumulator, and what is in it, to their common maximum.
+      float back = 0.f, own = 1.f;
+      if (folded) {
+        back = ex2_approx(fminf(m_sums - m, 0.f));
+        own = ex2_approx(fminf(m - m_sums, 0.f));
+        l = fmaf(l_sums, back, l * own);
+        m = fmaxf(m_sums, m);
+      }
       const bool has = j0 < s.count, has_other = C::WG == 2 && RT == 1 && (j0 ^ 1) < s.count;  // whether the streams had tiles of it
       if constexpr (C::WG == 2 && RT == 1) {
         // Each row's maxima and sums change hands while the last products run.
@@ -947,10 +956,10 @@ __global__ void __launch_bounds__(TreeCfg<D, RT>::THREADS, 1)
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
               const float4 y = sums[(c + e) / 4 * p.s.rows];
-              o[e] = __float_as_uint(fmaf(y.x, back, __uint_as_float(o[e])));
-              o[e + 1] = __float_as_uint(fmaf(y.y, back, __uint_as_float(o[e + 1])));
-              o[e + 2] = __float_as_uint(fmaf(y.z, back, __uint_as_float(o[e + 2])));
-              o[e + 3] = __float_as_uint(fmaf(y.w, back, __uint_as_float(o[e + 3])));
+              o[e] = __float_as_uint(fmaf(y.x, back, __uint_as_float(o[e]) * own));
+              o[e + 1] = __float_as_uint(fmaf(y.y, back, __uint_as_float(o[e + 1]) * own));
+              o[e + 2] = __float_as_uint(fmaf(y.z, back, __uint_as_float(o[e + 2]) * own));
+              o[e + 3] = __float_as_uint(fmaf(y.w, back, __uint_as_float(o[e + 3]) * own));
             }
           tmem_st32x32(o_at + c, o);
         }

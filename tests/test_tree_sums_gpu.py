@@ -4,6 +4,8 @@ import math
 import pytest
 import torch
 
+import scaled_dot_product_sdpa_gb300 as gb
+from reference64 import U, half_step
 from test_tree_gpu import _lib, call, problem  # noqa: F401 (_lib is a fixture)
 from tree_reference import attention, check_attention
 
@@ -21,3 +23,58 @@ def test_values_of_one_sign(B, d, Hq, T, old, least, most):
     v.copy_((torch.rand(v.shape, generator=torch.Generator().manual_seed(9)).double() * (most - least) + least).to(torch.bfloat16))
     got = call(q.cuda(), store.cuda(), view, table, lengths, counts, m)
     check_attention(got, attention(q, *view(store), table, lengths, counts, seen, 1 / math.sqrt(d)), max(lengths), d, "values of one sign", Hq * T)
+
+
+def one_row_a_cta(k, v, q, older, scale, short=False):
+    """attn_decode_tree's results for sequences of one key head, as many as CTAs (`short`: fewer, so that they are cut), all alike: tokens
+    `older` (numbers of pages of k, v [pages, page, d], one after the other) and then new ones, the last rows of k and v, as a
+    chain; q [Hq, T, d].  Beside it 64 bits: o, lse, and per element sum p |v|."""
+    Hq, T, d = q.shape
+    P, page, _ = k.shape
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    B = sms * 2 // 3 if short else sms
+    last = -(-T // page)
+    n = older.numel() * page + T
+    table = torch.cat([older.int(), torch.arange(P - last, P, dtype=torch.int32)]).cuda()[None].expand(B, -1)
+    got = gb.attn_decode_tree(q.cuda()[None].expand(B, -1, -1, -1).contiguous(), k.cuda()[:, None], v.cuda()[:, None], table, torch.full((B,), n, dtype=torch.int32, device="cuda"),
+                              scale=scale)
+    kd, vd, qd = (x.cuda().double() for x in (k, v, q))
+    times = torch.zeros(P, dtype=torch.float64).index_add_(0, older, torch.ones(older.numel(), dtype=torch.float64)).cuda()
+    x = scale * (qd @ kd.flatten(0, 1).T)  # [Hq, T, tokens of all pages]
+    fresh = scale * (qd @ kd[P - last:].flatten(0, 1)[:T].T)
+    S = scale * (qd.abs() @ kd.flatten(0, 1).abs().T).amax(-1)
+    x = torch.cat([x + times.log().repeat_interleave(page), torch.where(torch.ones(T, T, dtype=torch.bool).tril().cuda(), fresh, -math.inf)], -1)
+    p, values = torch.softmax(x, -1), torch.cat([vd.flatten(0, 1), vd[P - last:].flatten(0, 1)[:T]])
+    return got, p @ values, torch.logsumexp(x, -1), p @ values.abs(), S, n
+
+
+def rows_alike(got, o, lse, tol, lse_tol, what):
+    err = (got[0].double() - o).abs() / tol
+    assert (err <= 1).all(), f"{what}: o {err.max():.2f} times the tolerance, {(err > 1).double().mean():.4f} of the values beyond it"
+    err = (got[1].double() - lse).abs() / lse_tol
+    assert (err <= 1).all(), f"{what}: lse {err.max():.2f} times the tolerance"
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("d,n", [(64, 1 << 22), (128, 1 << 22), (256, 1 << 21), (512, 1 << 20)])
+@pytest.mark.parametrize("Hq,T", [(1, 2), (1, 40), (2, 90)])
+def test_long_tails_behind_few_large_weights(dtype, d, n, Hq, T):
+    """One token of each of the first two tiles has weight 1 and a value of zero, all others have weights of 2^-36.2, which fp16 cannot hold
+    beside it (scaled by 2^11: half the smallest number is 2^-36), and values that they alone decide.  All of these tails' weights are
+    alike, so that errors would not average out.
+    Tolerance of o, beside half a step: of sum p |v|, twice a logit's error ((d + 8) 2^-24 S), 2^-20 (the exponential, the sums), 2^-17 or half
+    a step of the type (weights), 2^-10 (sums that are cut off over up to 512 tiles); and in fp16, for the runs of up to 64 tiles that hold
+    the large weights, 2^-36 a token, of which a run has 2^13 and each of the two large weights one: 2^-23 of the largest value."""
+    page = 1 << 14
+    k, v = torch.zeros(3, page, d), (torch.rand(3, page, d, generator=torch.Generator().manual_seed(1)) + 1) * 3e4
+    k[0, [0, 128], 0] = 25.09
+    v[0, [0, 128]] = 0
+    q = torch.zeros(Hq, T, d)
+    q[..., 0] = 8
+    older = torch.cat([torch.zeros(1, dtype=torch.long), torch.ones(n // page - 1, dtype=torch.long)])
+    got, o, lse, size, S, n = one_row_a_cta(k.to(dtype), v.to(dtype), q.to(dtype), older, 0.125)
+    rows = Hq * T
+    logit = (d + 8) * U * S
+    share = 2 * logit + 2.0 ** -20 + (2.0 ** -17 if rows <= 32 else torch.finfo(dtype).eps / 2) + 2.0 ** -10
+    tol = half_step(dtype, o) + share[..., None] * size + (2.0 ** -23 * 6e4 if dtype == torch.float16 else 0)
+    rows_alike(got, o, lse, tol, logit + 2.0 ** -20 * (1 + lse.abs()), "tails")
