@@ -467,8 +467,8 @@ int attn_cache_keep(void *k_pages, void *v_pages, long long page_stride, long lo
  * enters its product with the values as the sum of two values of the cache's type, as in
  * attn_decode_paged (22 bits of it in fp16, 16 in bf16: by at most 2^-17 of itself); with more rows it is
  * rounded to that type, as in attn_fwd (by at most 2^-11 of itself in fp16, 2^-8 in bf16).  The products' sums
- * leave the tensor cores' accumulators, rounded to fp32, every 64 tiles of 128 tokens that one takes of a row in
- * fp16, every 512 in bf16.  Each such run of tiles has a maximum of its own, and that bounds how small a weight can be:
+ * leave the tensor cores' accumulators, rounded to fp32, every 8 tiles of 128 tokens that one takes of a row, with
+ * more rows every 64 in fp16 and 128 in bf16 (2^-17, 2^-14 and 2^-13 of a sum at most).  Each such run of tiles has a maximum of its own, and that bounds how small a weight can be:
  * in fp16, with few rows and with many, one below 2^-25 of its run's largest is off by up to 2^-36 of that (it is zero below 2^-36).
  * So these errors come to 2^-23 of the largest value at most and do not grow with the length, and neither do those of the sums.
  * One rounding to the output's type.  The same call gives the same bits.

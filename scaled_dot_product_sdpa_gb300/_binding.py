@@ -838,7 +838,7 @@ def attn_decode_tree(q, k_pages, v_pages, table, lengths, counts=None, mask=None
     piece of a prompt).  Rows behind counts, and rows that see nothing, give zeros and -inf.  Sums in float32; the weights that meet
     the values keep 22 bits with float16 and 16 with bfloat16 where a key head has up to 32 rows (Hq / Hkv * T), and are rounded
     to the cache's type, as in attn_fwd, where it has more; with float16 those below 2^-25 of the largest of the tokens that are summed
-    together (64 tiles of 128) are off by up to 2^-36 of it.  Values within a sequence's length are finite.  Outputs, and the
+    together (8 or 64 tiles of 128) are off by up to 2^-36 of it.  Values within a sequence's length are finite.  Outputs, and the
     workspace unless given (a contiguous CUDA tensor of attn_decode_tree_workspace_bytes bytes), are allocated by
     torch.  Enqueued on `stream`."""
     dev, code, (_, Hkv, _, d), cache = _cache(k_pages, v_pages)

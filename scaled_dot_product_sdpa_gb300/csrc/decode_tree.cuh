@@ -50,8 +50,17 @@ constexpr TreeShape tree_shape(int G, int T, int d) {
 // rows, 8 x 32 x 8192 keys 184 and 174.
 constexpr bool tree_split_weights(int G, int T) { return static_cast<long long>(G) * T <= 32; }
 
+// Tiles after which an accumulator's sums leave it.  The tensor cores add to it by cutting off what falls below its last bit, up to
+// 2^-23 of a sum a product (half of that where the sum grows evenly): every 8 tiles where the weights have two parts, as in
+// attn_decode_paged, so that the sums keep what those parts hold (8 x 8 products of the first parts, 2^-18 to 2^-17); where they are
+// rounded to 16 bits every 64 in fp16 (2^-15 to 2^-14) and 128 in bf16 (2^-14 to 2^-13), an eighth to a quarter and a 32nd to a 16th of a half
+// step.  GB300, with two parts every 8, 16 and 32 tiles: 8 x 32 x 8192 keys x 16 rows 171, 170 and 168 us, 131072 x 8 x 128 with 32 rows 94,
+// 92 and 91, 262144 x 8 x 64 134, 131 and 130, 65536 x 8 x 256 98, 95 and 92; with one, in bf16, every 64, 128 and 512: 1,048,576 x 128 rows
+// 650, 598 and 588, 2048 new tokens behind 65536 1940, 1838 and 1792.
+constexpr int tree_fold(int G, int T, bool bf16) { return tree_split_weights(G, T) ? 8 : bf16 ? 128 : 64; }
+
 // Workspace: a record per CTA, then two partial results per CTA, each of `tiles` row tiles' log-sum-exps (base 2) and o
-// (normalised, fp32), then the sums that leave the tensor cores' accumulators in long rows.
+// (normalised, fp32), then the sums that leave the tensor cores' accumulators in long rows (of up to 32 rows: in shared memory).
 struct TreeRecord {
   int b, kv, tu, x, cnt;  // the unit whose row tiles this CTA's last partial begins, and its sequence's new tokens
   int parts;              // partial results to join: this CTA's second, then the first of each of the following parts - 1 CTAs
@@ -62,8 +71,8 @@ constexpr int tree_streams(int d) { return d <= 128 ? 2 : 1; }           // accu
 constexpr long long tree_part_floats(const TreeShape &s, int d) { return static_cast<long long>(s.tiles) * s.rows * tree_columns(d); }
 constexpr long long tree_workspace_bytes(int G, int T, int d) {
   const TreeShape s = tree_shape(G, T, d);
-  return kTreeMaxCtas * (static_cast<long long>(sizeof(TreeRecord)) + 4LL * (2 * s.tiles * s.rows + 2 * tree_part_floats(s, d) +
-                                                                          static_cast<long long>(tree_streams(d)) * s.rows * tree_columns(d)));
+  const long long sums = tree_split_weights(G, T) ? 0 : static_cast<long long>(tree_streams(d)) * s.rows * tree_columns(d);
+  return kTreeMaxCtas * (static_cast<long long>(sizeof(TreeRecord)) + 4LL * (2 * s.tiles * s.rows + 2 * tree_part_floats(s, d) + sums));
 }
 
 struct TreeParams {

@@ -6,10 +6,9 @@
 //     S [128 rows x 128 keys] = Q K^T,   O [128 rows x d] += P V,   P from tensor memory, over its S.
 // Weights enter the second product (in fp16 times 2^11, in bf16 times 2^-40, see kShift) of up to 32 rows as two 16-bit parts, P = hi + lo,
 // over twice the keys (that keeps 16 bits in bf16, 22 in fp16), of more rows rounded to the cache's type (see
-// tree_split_weights).  The tensor cores add to an fp32 accumulator by cutting off what falls below its last bit, about 2^-24
-// of a sum a product: so a sum leaves its accumulator every `fold` tiles (2^-15 to 2^-14 in fp16, 2^-12 to 2^-11 in bf16, an
-// eighth to a quarter of the result's half step), for a place in the workspace where it is added to in fp32, rounded to
-// nearest, and the weights' sum with it.  Each such run of tiles goes by its own maximum, so that a weight's last bit is one of that
+// tree_split_weights).  The tensor cores add to an fp32 accumulator by cutting off what falls below its last bit: so
+// a sum leaves its accumulator every `fold` tiles (see tree_fold), for a place in shared memory (up to 32 rows) or the workspace where it is
+// added to in fp32, rounded to nearest, and the weights' sum with it.  Each such run of tiles goes by its own maximum, so that a weight's last bit is one of that
 // run's, however long the row is (in fp16 weights below 2^-25 of the maximum are subnormal, kept to 2^-36 of it).
 //
 // d <= 128: two accumulator sets ("streams"), each an S tile, an O tile and a softmax warpgroup of its own,
@@ -82,7 +81,7 @@ struct TreeCfg {
   static constexpr int EXCHANGE_BYTES = WG == 2 && RT == 1 ? 2 * 2 * 128 * 4 : 0;  // the streams' maxima and sums
   static constexpr int BAR_BYTES = 768;                 // barriers, the tiles' and the segments' words
   static constexpr int SMEM_MOST = 232448;
-  static constexpr int ROOM = SMEM_MOST - PAGE_BYTES - EXCHANGE_BYTES - BAR_BYTES;  // queries and ring
+  static constexpr int ROOM = SMEM_MOST - PAGE_BYTES - EXCHANGE_BYTES - BAR_BYTES;  // queries, ring and sums
   // barriers
   static constexpr int B_FULL = 0, B_EMPTY = MAX_SLOTS, B_QFULL = 2 * MAX_SLOTS, B_QEMPTY = B_QFULL + 2, B_SFULL = B_QEMPTY + 2, B_PFULL = B_SFULL + 2,
                        B_PDONE = B_PFULL + 2, B_DRAIN = B_PDONE + 2, B_MEET = B_DRAIN + 1, B_SEG = B_MEET + 1, NBAR = B_SEG + kTreeSegs;
@@ -311,8 +310,9 @@ __global__ void __launch_bounds__(TreeCfg<D, RT>::THREADS, 1)
   const uint32_t NSLOT = p.slots;
   const int NQB = p.q_buffers;
   const uint32_t q_tile = static_cast<uint32_t>(p.s.q_rows) * 128u * (D / 64), q_bytes = q_tile * RT;  // of a row tile, of a unit
-  // Queries, ring, page numbers, exchange, barriers.  (A product reads 128 rows of queries from each box: behind the last one, the ring.)
-  const uint32_t ring = q_bytes * static_cast<uint32_t>(NQB), off_pages = ring + NSLOT * C::SLOT_BYTES;
+  // Queries, ring, sums, page numbers, exchange, barriers.  (A product reads 128 rows of queries from each box: behind the last one, the ring.)
+  const uint32_t ring = q_bytes * static_cast<uint32_t>(NQB), off_sums = ring + NSLOT * C::SLOT_BYTES;
+  const uint32_t off_pages = off_sums + (LO ? static_cast<uint32_t>(C::WG * C::DV * 4 * p.s.q_rows) : 0u);
   const uint32_t off_exchange = off_pages + C::PAGE_BYTES, off_bars = off_exchange + C::EXCHANGE_BYTES;
   float *const exchange = reinterpret_cast<float *>(base_ptr + off_exchange);  // [maximum, sum][stream][row]
   // (Rounded up to 16 bytes for the segments' words.)
@@ -699,8 +699,11 @@ __global__ void __launch_bounds__(TreeCfg<D, RT>::THREADS, 1)
     auto met = [&]() { wait(C::B_MEET, meetings++); };
     const int row_tile = RT == 2 ? stream : 0;
     const int heads_row = r / p.s.tokens, token_row = r - heads_row * p.s.tokens;
-    // Of this stream, this row: four columns of all rows lie side by side, so that a warp's stores fill whole lines.
-    float4 *const sums = reinterpret_cast<float4 *>(p.sums) + (static_cast<long long>(blockIdx.x) * C::WG + stream) * (C::DV / 4) * p.s.rows + r;
+    // Of this stream, this row: four columns of all rows lie side by side, so that a warp's stores fill whole lines.  Those of up to 32
+    // rows are in shared memory: a look at the workspace waits behind the ring's loads for 2 to 3 us.
+    const int sums_step = LO ? p.s.q_rows : p.s.rows;
+    float4 *const sums = (LO ? reinterpret_cast<float4 *>(base_ptr + off_sums) + stream * (C::DV / 4) * sums_step
+                             : reinterpret_cast<float4 *>(p.sums) + (static_cast<long long>(blockIdx.x) * C::WG + stream) * (C::DV / 4) * sums_step) + r;
     uint32_t steps = 0, ends = 0, ends_other = 0;  // S tiles of this stream, ends of segments of this and of the other one
     uint32_t g = 0;                // tiles of the share before the segment
     struct {
@@ -833,10 +836,10 @@ __global__ void __launch_bounds__(TreeCfg<D, RT>::THREADS, 1)
                     for (int e = 0; e < 32; e += 4) {
                       float4 x = make_float4(__uint_as_float(o[e]) * add, __uint_as_float(o[e + 1]) * add, __uint_as_float(o[e + 2]) * add, __uint_as_float(o[e + 3]) * add);
                       if (folded) {
-                        const float4 y = sums[(c + e) / 4 * p.s.rows];
+                        const float4 y = sums[(c + e) / 4 * sums_step];
                         x = make_float4(fmaf(y.x, keep, x.x), fmaf(y.y, keep, x.y), fmaf(y.z, keep, x.z), fmaf(y.w, keep, x.w));
                       }
-                      sums[(c + e) / 4 * p.s.rows] = x;
+                      sums[(c + e) / 4 * sums_step] = x;
                     }
                 }
                 l_sums = fmaf(l_sums, keep, l * add);  // (the weights' sum, too: in one number each tile of a row of 2^31 would be rounded to 2^-8)
@@ -955,7 +958,7 @@ __global__ void __launch_bounds__(TreeCfg<D, RT>::THREADS, 1)
           if (valid)
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-              const float4 y = sums[(c + e) / 4 * p.s.rows];
+              const float4 y = sums[(c + e) / 4 * sums_step];
               o[e] = __float_as_uint(fmaf(y.x, back, __uint_as_float(o[e]) * own));
               o[e + 1] = __float_as_uint(fmaf(y.y, back, __uint_as_float(o[e + 1]) * own));
               o[e + 2] = __float_as_uint(fmaf(y.z, back, __uint_as_float(o[e + 2]) * own));
@@ -1117,11 +1120,11 @@ cudaError_t launch_tree_as(const TreeLaunch &a) {
     if (dev < 64) configured |= 1ull << dev;
   }
   TreeParams p = a.p;
-  // Queries of two units where the ring keeps five slots of 32 KB beside them.
-  const int q_bytes = p.s.q_rows * 2 * D * RT;
-  p.q_buffers = (C::ROOM - 2 * q_bytes) / C::SLOT_BYTES >= (D == 64 ? 10 : 5) ? 2 : 1;
-  p.slots = std::min(C::MAX_SLOTS, (C::ROOM - p.q_buffers * q_bytes) / C::SLOT_BYTES);
-  const int smem = p.q_buffers * q_bytes + p.slots * C::SLOT_BYTES + C::PAGE_BYTES + C::EXCHANGE_BYTES + C::BAR_BYTES;
+  // Queries of two units where the ring keeps five slots of 32 KB beside them and the sums.
+  const int q_bytes = p.s.q_rows * 2 * D * RT, sums_bytes = LO ? C::WG * C::DV * 4 * p.s.q_rows : 0, room = C::ROOM - sums_bytes;
+  p.q_buffers = (room - 2 * q_bytes) / C::SLOT_BYTES >= (D == 64 ? 10 : 5) ? 2 : 1;
+  p.slots = std::min(C::MAX_SLOTS, (room - p.q_buffers * q_bytes) / C::SLOT_BYTES);
+  const int smem = p.q_buffers * q_bytes + p.slots * C::SLOT_BYTES + sums_bytes + C::PAGE_BYTES + C::EXCHANGE_BYTES + C::BAR_BYTES;
   // At most one CTA per tile that the tables have room for (and lengths, of 31 bits, can name).
   const long long row_tiles =
       std::min((static_cast<long long>(p.table_w) * p.page + kTreeTile - 1) / kTreeTile, (1LL << 31) / kTreeTile);

@@ -611,7 +611,7 @@ extern "C" int attn_decode_tree(const void *q, long long q_sb, long long q_sh, l
   p.tile_pages = kTreeTile / page;
   p.tile_slots = kTreeTile % page;
   p.bf16 = dtype == GBATTN_BF16;
-  p.fold = p.bf16 ? 512 : 64;
+  p.fold = tree_fold(p.G, T, p.bf16);
   p.c2 = scale * 1.4426950408889634f;
   p.o = o;
   p.lse = lse;

@@ -78,3 +78,71 @@ def test_long_tails_behind_few_large_weights(dtype, d, n, Hq, T):
     share = 2 * logit + 2.0 ** -20 + (2.0 ** -17 if rows <= 32 else torch.finfo(dtype).eps / 2) + 2.0 ** -10
     tol = half_step(dtype, o) + share[..., None] * size + (2.0 ** -23 * 6e4 if dtype == torch.float16 else 0)
     rows_alike(got, o, lse, tol, logit + 2.0 ** -20 * (1 + lse.abs()), "tails")
+
+
+# Up to 32 rows of a key head, 33 to 128, more (d <= 128: two row tiles that share each key tile).
+ROWS = [(4, 6), (2, 30), (1, 140)]
+
+
+def run_of(rows, dtype):
+    """Tiles whose sums stay in an accumulator."""
+    return 8 if rows <= 32 else 64 if dtype == torch.float16 else 128
+
+
+def half_a_step(dtype, value, off):
+    """The largest error of rounding a number within `off` of `value` (both normal): half the distance of its neighbours, not of a power of two's."""
+    return torch.exp2(torch.floor(torch.log2(value.abs() + off))) * (torch.finfo(dtype).eps / 2)
+
+
+def values(shape, g):
+    """Values around a mean of each column's own, below 2 (so that the results lie anywhere between two numbers of their type)."""
+    return (1.6 + 0.3 * torch.rand(shape[-1], generator=g)) * (1 + 0.05 * torch.randn(shape, generator=g))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("d", [64, 128, 256, 512])
+@pytest.mark.parametrize("Hq,T", ROWS)
+@pytest.mark.parametrize("short", [False, True])
+def test_weights_of_powers_of_two_over_many_tiles(dtype, d, Hq, T, short):
+    """Weights of 1, 1/2, ... 2^-14, drawn at random: each fits its type, so that o is off by what its sums lose, and products with 8 or 11 bits
+    of a value reach below the sums' last bits.
+    Tolerance beside half a step, of sum p |v| (v > 0): a run's 16 products a tile (8 where weights have one part) are cut off by up
+    to 2^-23 of the sum at the time, whose mean is half of the run's; the sums of values and of weights are rounded to nearest where a run's
+    joins them, 2^-24 of what there is, half of that in the mean; 2^-20 for the rest (an exponent is off by up to 14 2^-24)."""
+    page, tiles = 1 << 10, 1104
+    g = torch.Generator().manual_seed(d + T)
+    k, v = torch.zeros(9, page, d), values((9, page, d), g)
+    k[..., 0] = -torch.randint(0, 15, (9, page), generator=g)
+    q = torch.zeros(Hq, T, d)
+    q[..., 0] = 8
+    older = torch.arange(8).repeat(tiles // 64)
+    scale = float(torch.tensor(math.log(2) / 8, dtype=torch.float32))
+    got, o, lse, size, S, n = one_row_a_cta(k.to(dtype), v.to(dtype), q.to(dtype), older, scale, short)
+    rows, run = Hq * T, run_of(Hq * T, dtype)
+    turns = tiles / 2 if d <= 128 and rows <= 128 else tiles
+    off = (run * (16 if rows <= 32 else 8) * U + turns / run * U + 2.0 ** -20) * size
+    rows_alike(got, o, lse, half_a_step(dtype, o, off) + off, 2.0 ** -20 * (1 + lse.abs()), "powers of two")
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("d", [64, 128, 256, 512])
+@pytest.mark.parametrize("Hq,T", ROWS)
+@pytest.mark.parametrize("short", [False, True])
+def test_maxima_that_rise_and_fall_over_many_tiles(dtype, d, Hq, T, short):
+    """Logits of about +-12 that change from page to page, 64 pages in an order drawn at random: runs of tiles whose maxima lie far apart, in
+    either order.  Tolerance, beside half a step: of sum p |v|, twice a logit's error, 2^-20 (the exponential), the weights' rounding, 16 products a
+    tile of a run (8 where the weights have one part) cut off by 2^-23 of its sum each, and all sums' roundings to nearest (32 weights one after
+    the other, moves of the maximum in a run, runs); in fp16 the floor of small weights, 2^-36 a token of a run: 2^-23 of the largest value."""
+    page, tiles = 1 << 10, 400
+    g = torch.Generator().manual_seed(d + T)
+    k, v = 0.3 * torch.randn(65, page, d, generator=g), values((65, page, d), g)
+    k[..., 0] = 24 * torch.rand(65, 1, generator=g) - 12
+    q = torch.randn(Hq, T, d, generator=g)
+    q[..., 0] = 8
+    older = torch.randint(0, 64, (tiles // 8,), generator=g)
+    got, o, lse, size, S, n = one_row_a_cta(k.to(dtype), v.to(dtype), q.to(dtype), older, 0.125, short)
+    rows, run = Hq * T, run_of(Hq * T, dtype)
+    logit, rounded = (d + 8) * U * S, 2 * (32 + run + tiles / run) * U
+    share = 2 * logit + 2.0 ** -20 + (2.0 ** -17 if rows <= 32 else torch.finfo(dtype).eps / 2) + run * (16 if rows <= 32 else 8) * 2 * U + rounded
+    off = share[..., None] * size + (2.0 ** -23 * 4 if dtype == torch.float16 else 0)
+    rows_alike(got, o, lse, half_a_step(dtype, o, off) + off, logit + 2.0 ** -20 * (1 + lse.abs()) + rounded, "moving maxima")
