@@ -470,8 +470,8 @@ int attn_cache_keep(void *k_pages, void *v_pages, long long page_stride, long lo
  * leave the tensor cores' accumulators, rounded to fp32, every 8 tiles of 128 tokens that one takes of a row, with
  * more rows every 64 in fp16 and 128 in bf16 (2^-17, 2^-14 and 2^-13 of a sum at most).  Each such run of tiles has a maximum of its own, and that bounds how small a weight can be:
  * in fp16, with few rows and with many, one below 2^-25 of its run's largest is off by up to 2^-36 of that (it is zero below 2^-36).
- * So these errors come to 2^-23 of the largest value at most and do not grow with the length, and neither do those of the sums.
- * One rounding to the output's type.  The same call gives the same bits.
+ * So these errors come to 2^-23 of the largest value at most, however long the row is; the runs' sums are added up in fp32, each
+ * rounded to nearest.  One rounding to the output's type.  The same call gives the same bits.
  */
 int attn_decode_tree(const void *q, long long q_sb, long long q_sh, long long q_sl, const void *k_pages,
                      const void *v_pages, long long page_stride, long long head_stride, long long slot_stride, int pages,

@@ -514,11 +514,15 @@ __global__ void __launch_bounds__(TreeCfg<D, RT>::THREADS, 1)
         TreeRecord record = {};
         Walk w(p, start);
         Seg q;
-        int s = 0;
+        int s = 0, held[2] = {0, 0};  // tiles of the segments whose queries are in the buffers
         for (; ok && w.next(q); ++s) {
           const int buf = NQB == 1 ? 0 : s & 1, turn = NQB == 1 ? s : s >> 1;
-          if (turn > 0) ok = wait_bounded(BAR(C::B_QEMPTY + buf), (turn - 1) & 1, &misc.abort_flag, p.status, kDevTimeoutLoad, p.wait_limit);
+          // This wait may last for a whole segment, so that it gets a limit for each of its tiles (the others' waits, of a tile at
+          // most, run out first where something is wrong, and end this one too).
+          if (turn > 0)
+            ok = wait_bounded(BAR(C::B_QEMPTY + buf), (turn - 1) & 1, &misc.abort_flag, p.status, kDevTimeoutLoad, p.wait_limit * (buf ? held[1] : held[0]));
           if (!ok) break;
+          if (buf) held[1] = q.count; else held[0] = q.count;
           // The words of the segment kTreeSegs before are past: the QK of the segment NQB before is done, so the PVs of all tiles but
           // its last two are, and both warpgroups have come to those.
           const bool whole = q.count == q.tiles, begins = q.tile == 0;

@@ -25,14 +25,14 @@ def test_values_of_one_sign(B, d, Hq, T, old, least, most):
     check_attention(got, attention(q, *view(store), table, lengths, counts, seen, 1 / math.sqrt(d)), max(lengths), d, "values of one sign", Hq * T)
 
 
-def one_row_a_cta(k, v, q, older, scale, short=False):
-    """attn_decode_tree's results for sequences of one key head, as many as CTAs (`short`: fewer, so that they are cut), all alike: tokens
+def one_row_a_cta(k, v, q, older, scale, short=False, more=0):
+    """attn_decode_tree's results for sequences of one key head, as many as CTAs (`short`: fewer, so that they are cut; and `more`), all alike: tokens
     `older` (numbers of pages of k, v [pages, page, d], one after the other) and then new ones, the last rows of k and v, as a
     chain; q [Hq, T, d].  Beside it 64 bits: o, lse, and per element sum p |v|."""
     Hq, T, d = q.shape
     P, page, _ = k.shape
     sms = torch.cuda.get_device_properties(0).multi_processor_count
-    B = sms * 2 // 3 if short else sms
+    B = (sms * 2 // 3 if short else sms) + more
     last = -(-T // page)
     n = older.numel() * page + T
     table = torch.cat([older.int(), torch.arange(P - last, P, dtype=torch.int32)]).cuda()[None].expand(B, -1)
