@@ -379,9 +379,11 @@ int attn_cache_copy(void *k_pages, void *v_pages, long long page_stride, long lo
  * What lies behind a sequence's last token in its last page does not matter (NaN included).
  * Arithmetic: logits, maxima and sums in fp32; the products of weights and values run on the tensor
  * cores with each weight as the sum of two values of the cache's type, so with 22 of its bits in
- * fp16 and 16 in bf16 (2^-17 of it at most); their sums are rounded to fp32 every 1024 tokens, so
- * that no error grows with the length; one rounding to the output's type.  The same call gives
- * the same bits.
+ * fp16 and 16 in bf16 (2^-17 of it at most; in fp16 one below 2^-27 of its row's largest so far is off by up to
+ * 2^-38 of that, so that a tail of n such tokens comes to n 2^-38); their sums are rounded to fp32 every 1024 tokens;
+ * one rounding to the output's type.  The same call gives the same bits.  Weights are kept times 2^13: the sum of a
+ * row's weights (the largest of them 1 to 4) times 2^13 times its largest value has to stay below 2^128 (in bf16: values of
+ * up to 4e30 where the weights' sum is 10^4).
  */
 int attn_decode_paged(const void *q, long long q_sb, long long q_sh, const void *k_pages, const void *v_pages,
                       long long page_stride, long long head_stride, long long slot_stride, int pages, int page,
@@ -466,12 +468,14 @@ int attn_cache_keep(void *k_pages, void *v_pages, long long page_stride, long lo
  * Arithmetic: logits, maxima and sums in fp32.  Where a key head has up to 32 rows (Hq / Hkv * T) each weight
  * enters its product with the values as the sum of two values of the cache's type, as in
  * attn_decode_paged (22 bits of it in fp16, 16 in bf16: by at most 2^-17 of itself); with more rows it is
- * rounded to that type, as in attn_fwd (by at most 2^-11 of itself in fp16, 2^-8 in bf16).  The products' sums
- * leave the tensor cores' accumulators, rounded to fp32, every 8 tiles of 128 tokens that one takes of a row, with
- * more rows every 64 in fp16 and 128 in bf16 (2^-17, 2^-14 and 2^-13 of a sum at most).  Each such run of tiles has a maximum of its own, and that bounds how small a weight can be:
- * in fp16, with few rows and with many, one below 2^-25 of its run's largest is off by up to 2^-36 of that (it is zero below 2^-36).
- * So these errors come to 2^-23 of the largest value at most, however long the row is; the runs' sums are added up in fp32, each
- * rounded to nearest.  One rounding to the output's type.  The same call gives the same bits.
+ * rounded to that type, as in attn_fwd (by at most 2^-11 of itself in fp16, 2^-8 in bf16).  The
+ * products' sums leave the tensor cores' accumulators, rounded to fp32, every 8 tiles of 128 tokens
+ * that one takes of a row, with more rows every 64 in fp16 and 128 in bf16 (2^-16, 2^-14 and 2^-13 of
+ * a sum at most).  Each such run of tiles has a maximum of its own, and that bounds how small a weight
+ * can be: in fp16, with few rows and with many, one below 2^-25 of its run's largest is off by up to
+ * 2^-36 of that (it is zero below 2^-36), in bf16 one below 2^-86 may be zero. So these errors come to
+ * 2^-23 of the largest value at most, however long the row is; the runs' sums are added up in fp32,
+ * each rounded to nearest.  One rounding to the output's type.  The same call gives the same bits.
  */
 int attn_decode_tree(const void *q, long long q_sb, long long q_sh, long long q_sl, const void *k_pages,
                      const void *v_pages, long long page_stride, long long head_stride, long long slot_stride, int pages,

@@ -44,15 +44,16 @@ constexpr TreeShape tree_shape(int G, int T, int d) {
 }
 
 // Whether weights enter the second product as two 16-bit parts, or rounded to 16 bits.  With few rows of a key head (a few
-// drafts) the parts cost little, and a verified token's row keeps the bits that attn_decode_paged gives it.  With many the
-// products bound the kernel, by their time and, in a long run, by their power (clocks of 1.4 GHz instead of 2.07): GB300, both
-// parts and one, 128 rows, 1,048,576 x 8 keys x 128 728 and 609 us, 256 rows and more 2048 new tokens of 4 prompts 764 and 656; 16
-// rows, 8 x 32 x 8192 keys 184 and 174.
+// drafts) a verified token's row keeps the bits that attn_decode_paged gives it, and mostly at a small price: GB300, both parts (with sums
+// in shared memory) and one, 16 rows, 8 x 32 x 8192 keys 175 and 171 us, 32 rows, 131072 x 8 x 128 96 and 91, 65536 x 8 x 256 98 and 92, but
+// 262144 x 8 x 64 134 and 106.  With many the products bound the kernel, by their time and, in a long run, by their power (clocks of
+// 1.4 GHz instead of 2.07): 128 rows, 1,048,576 x 8 keys x 128 728 and 609 us, 2048 new tokens of 4 prompts 764 and 656 (with sums in
+// the workspace every 64 or 512 tiles; those of 128 rows would not fit shared memory).
 constexpr bool tree_split_weights(int G, int T) { return static_cast<long long>(G) * T <= 32; }
 
 // Tiles after which an accumulator's sums leave it.  The tensor cores add to it by cutting off what falls below its last bit, up to
 // 2^-23 of a sum a product (half of that where the sum grows evenly): every 8 tiles where the weights have two parts, as in
-// attn_decode_paged, so that the sums keep what those parts hold (8 x 8 products of the first parts, 2^-18 to 2^-17); where they are
+// attn_decode_paged, so that the sums keep about what those parts hold (16 products a tile, 2^-17 to 2^-16); where they are
 // rounded to 16 bits every 64 in fp16 (2^-15 to 2^-14) and 128 in bf16 (2^-14 to 2^-13), an eighth to a quarter and a 32nd to a 16th of a half
 // step.  GB300, with two parts every 8, 16 and 32 tiles: 8 x 32 x 8192 keys x 16 rows 171, 170 and 168 us, 131072 x 8 x 128 with 32 rows 94,
 // 92 and 91, 262144 x 8 x 64 134, 131 and 130, 65536 x 8 x 256 98, 95 and 92; with one, in bf16, every 64, 128 and 512: 1,048,576 x 128 rows

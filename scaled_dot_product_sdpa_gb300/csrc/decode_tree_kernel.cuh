@@ -28,11 +28,11 @@
 // the seven others (as first written, 147 us where 93 are taken now, a third of all issue slots waited for instructions).
 //
 // Measured on GB300 (131072 tokens x 8 key heads x 128, bf16, pages of 16; 537 MB, floor 79 us, of which 8 to 11 are launch,
-// first tile and join): 16 or 32 rows a key head 89 us, 64 92, 128 93 (5.8 TB/s; a longer row runs at 7.2 TB/s), 256 119
-// (1160 TFLOP/s), 512 217 (1268).  The same bytes at d = 64 113, bound by the issuer's turn of twelve products a tile; at 256
-// 98; at 512 with 64 rows 134 (K is read for each half of V's columns), with 128 246 (and again for each 64 rows).  Pages of 8
-// 107: a producer issues a box of 8 rows in about 94 cycles.  One sequence of 1000 tokens 11 us; 200 of 50 to
-// 300 tokens, 32/8 heads x 4 tokens, 102: a unit of two tiles is a chain of two softmaxes, two products and a result.
+// first tile and join): 16 or 32 rows a key head 92 to 93 us, 64 92, 128 94 (5.7 TB/s; a longer row runs at 7.0 TB/s), 256 121
+// (1140 TFLOP/s), 512 222 (1237).  The same bytes at d = 64 117, bound by the issuer's turn of twelve products a tile (with 32 rows
+// 133: twenty); at 256 98 to 99; at 512 with up to 64 rows 132 to 134 (K is read for each half of V's columns), with 128 247 (and again
+// for each 64 rows).  Pages of 8 109: a producer issues a box of 8 rows in about 94 cycles.  One sequence of 1000 tokens 11 us; 200 of
+// 50 to 300 tokens, 32/8 heads x 4 tokens, 106: a unit of two tiles is a chain of two softmaxes, two products and a result, which explains half of it.
 #pragma once
 
 #include <atomic>
@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(TreeCfg<D, RT>::THREADS, 1)
           bool made = false;
           if constexpr (RT == 2 && D == 64) {
             // Weights by the maximum so far, of logits that are read once; seldom is it left behind, and they are made again.  2048 new
-            // tokens behind 6144, 32/8 heads x 64 179 -> 165 us.  Not at 128, where the issuer's turns bound the kernel (4 x 2048 new
+            // tokens behind 6144, 32/8 heads x 64 179 -> 165 us (both before bf16's scale, 172 with it).  Not at 128, where the issuer's turns bound the kernel (4 x 2048 new
             // tokens 503 -> 512), nor for one row tile, where more code costs what it saves (pages of 128 106 -> 96, of 16 51 -> 52).
             if (!edge && turn > 0 && !fold) {
               const float from = m == -INFINITY ? 0.f : m - kShift<BF>;

@@ -9,7 +9,8 @@ def attn_tree_mask(parents) -> tuple[torch.Tensor, torch.Tensor]:
     for one that follows the older tokens directly.  A token sees itself and all that it follows.  Returns int32 words
     [..., T, (T + 31) // 32] (bit j % 32 of word j // 32 of row t: whether t sees j) and int32 depths [..., T] (0 without a parent):
     a token's rotary position is that of the first new token plus its depth.  On the device of `parents` (a tensor, or
-    nested lists: the CPU).  A tree's shape is known before its tokens are, so this is meant to run once, not every step."""
+    nested lists: the CPU).  The check of the parents reads one result back, and the rest is a loop over T in Python: on a GPU it waits for that and
+    cannot be captured.  A tree of fixed shape needs it once; one that is chosen anew each step gets its masks outside the captured part."""
     parents = torch.as_tensor(parents)
     if parents.dim() < 1 or parents.shape[-1] < 1 or parents.dtype.is_floating_point or parents.dtype == torch.bool:
         raise ValueError("gbattn: parents must be whole numbers [..., T], T > 0")
